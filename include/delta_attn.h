@@ -15,6 +15,10 @@
  *   delta_select_attn  full decode attention + per-page scores + page selection (delta-layers)
  *   delta_sparse_attn  decode attention over the selected pages only (sparse layers);
  *                      delta_sparse_attn_settled when the selection was final one kernel earlier
+ *   delta_window_attn  decode attention over the first tokens (sinks) and the last ones (window)
+ *   delta_rope         rotary positions of q and k, before the append
+ *   delta_*_q8         the same steps over a cache held in 8 bits with a scale per block, and
+ *                      its bulk write and read back
  *
  * Conventions shared by every call
  * --------------------------------
@@ -224,6 +228,140 @@ delta_status delta_sparse_attn_settled(const delta_desc* desc, const delta_page_
                                        const int32_t* sel_cnt, const int32_t* sel_pages, int32_t sel_stride,
                                        const void* q, const void* k_pool, const void* v_pool, void* o,
                                        void* workspace, size_t ws_bytes, void* stream);
+
+/* Window layer: decode attention over the tokens t < sink_tokens and t >= kv_len[b] - window_tokens
+ * (each token once; the newest token is visible when window_tokens >= 1).  Both counts are >= 0; a
+ * sequence with no visible token (kv_len 0, or both counts 0) gives o = 0.  Reads only the pages
+ * that hold a visible token; a hidden token's K and V may hold anything.  Same workspace
+ * (delta_workspace_size) and device flags as delta_full_attn. */
+delta_status delta_window_attn(const delta_desc* desc, const delta_page_table* pt, int32_t window_tokens,
+                               int32_t sink_tokens, const void* q, const void* k_pool, const void* v_pool,
+                               void* o, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ rotary positions
+ * Pair j of a head (j < rotary_dim/2) turns by 2*pi * position * turns[j] and is scaled by
+ * magnitude; the other dimensions pass through:
+ *   a' = magnitude * (a cos - b sin),  b' = magnitude * (b cos + a sin).
+ * DELTA_ROPE_HALF pairs dimensions (j, j + rotary_dim/2), DELTA_ROPE_INTERLEAVED (2j, 2j + 1). */
+typedef enum { DELTA_ROPE_HALF = 0, DELTA_ROPE_INTERLEAVED = 1 } delta_rope_layout;
+
+/* Frequencies for contexts longer than the trained one (f_j = base^(-2j/rotary_dim) radians a token):
+ *   DELTA_ROPE_PLAIN   f_j
+ *   DELTA_ROPE_LINEAR  f_j / factor (every position is divided by factor)
+ *   DELTA_ROPE_BANDS   by the turns r_j = original_len * f_j / (2 pi) a pair makes over the trained
+ *                      context: f_j / factor below low_turns, f_j above high_turns, mixed linearly
+ *                      in r_j between (w f_j + (1 - w) f_j / factor, w = (r_j - low) / (high - low)) */
+typedef enum { DELTA_ROPE_PLAIN = 0, DELTA_ROPE_LINEAR = 1, DELTA_ROPE_BANDS = 2 } delta_rope_scaling;
+
+typedef struct {
+    int32_t rotary_dim;       /* even, >= 2 */
+    int32_t scaling;          /* delta_rope_scaling */
+    double  base;             /* > 1 */
+    double  factor;           /* >= 1; LINEAR and BANDS */
+    double  original_len;     /* > 0; BANDS */
+    double  low_turns;        /* >= 0; BANDS */
+    double  high_turns;       /* > low_turns; BANDS */
+} delta_rope_params;
+
+/* The table of delta_rope (a HOST function: plain host arrays, no GPU work): turns_out[j] =
+ * f_j / (2 pi), j < rotary_dim/2, in double precision.  The caller copies it to the device once. */
+delta_status delta_rope_table(const delta_rope_params* params, double* turns_out);
+
+typedef struct {
+    const double*  turns;         /* device, [rotary_dim/2] turns a token */
+    int32_t        rotary_dim;    /* even, 2..head_dim: the first dimensions of each head */
+    int32_t        layout;        /* delta_rope_layout */
+    float          magnitude;     /* finite; 1 for a plain rotation */
+    const int32_t* positions;     /* device, [num_positions] */
+    int32_t        num_positions; /* >= 1 */
+    int32_t        offset;        /* row r is at position positions[r % num_positions] + offset */
+} delta_rope_plan;
+
+/* Rotate `rows` rows of q [rows][num_q_heads][head_dim] and of k [rows][num_kv_heads][head_dim] (either
+ * may be NULL with its output: skipped).  With positions = kv_len, num_positions = batch and offset -1
+ * the rows [layers][batch] of a decode step are at their newest token's position; a prompt passes its
+ * rows' positions and offset 0.  Angles are formed in double precision, so far positions keep theirs.
+ * Strides: elements from row to row (a multiple of 16 bytes; 0 = heads * head_dim), at least heads *
+ * head_dim; rows of q_out and k_out likewise.  An output may be its input (same pointer and stride);
+ * otherwise the two must not overlap.  desc supplies heads, head_dim and dtype. */
+delta_status delta_rope(const delta_desc* desc, const delta_rope_plan* rope, int64_t rows,
+                        const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                        const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/* ------------------------------------------------------------------ the cache held in 8 bits
+ * A block is the 16 tokens of one (page, KV head) of K or of V: 16 * head_dim 8-bit values and one fp32
+ * scale; a value stands for payload * scale.  Scales are powers of two, 2^e with e the smallest
+ * integer >= -100 such that the block's largest magnitude is at most QMAX * 2^e (QMAX 448 for e4m3, 127
+ * for int8), so scaling is exact, a value is rounded once (to nearest even), and both formats read
+ * back exactly in bf16 and fp32.
+ * Tokens written into a block that already holds older tokens keep the larger of its scale and their
+ * own; when the scale grows, the older values are rounded again to the new one.  Growth at least
+ * doubles a step, so all roundings of a value together stay below one step of its block's scale.
+ * Writing the first slot of a page starts its blocks anew.
+ * A non-finite value makes its block's scale NaN until the block starts anew (every value of the block
+ * then reads as NaN): it shows in the output as it would in an unquantised cache. */
+typedef enum { DELTA_E4M3 = 0, DELTA_INT8 = 1 } delta_q8_format;
+
+typedef struct {
+    void*   k_pool;     /* [num_phys_pages][num_kv_heads][16][head_dim] 8-bit values */
+    void*   v_pool;
+    float*  k_scale;    /* [num_phys_pages][num_kv_heads] */
+    float*  v_scale;
+    int32_t format;     /* delta_q8_format */
+} delta_q8_cache;
+
+/* delta_kv_append and delta_kv_append_layers into the 8-bit cache (k_new, v_new in desc's dtype; in the
+ * second, caches is a HOST array of num_layers descriptors of one format).  Besides the token's slot they
+ * may rewrite the older tokens of its block and its scale. */
+delta_status delta_kv_append_q8(const delta_desc* desc, const delta_page_table* pt, const void* k_new,
+                                const void* v_new, const delta_q8_cache* cache, void* stream);
+delta_status delta_kv_append_layers_q8(const delta_desc* desc, const delta_page_table* pt, int32_t num_layers,
+                                       const void* const* k_new, const void* const* v_new,
+                                       const delta_q8_cache* caches, void* stream);
+
+/* Write many tokens at once (a prompt or a chunk of one): the last m_b = token_indptr[b+1] -
+ * token_indptr[b] tokens of each sequence, positions kv_len[b] - m_b .. kv_len[b] - 1, from rows
+ * token_indptr[b] + i of k and v ([tokens][num_kv_heads][head_dim] in desc's dtype; row_stride elements from
+ * row to row, a multiple of 16 bytes, 0 = contiguous).  token_indptr [batch+1] is device memory; max_tokens
+ * is the host's bound on m_b (it sizes the launch; a larger m_b is written all the same).  A page must
+ * belong to one sequence only while it is written.  Slots past the last token are left as they were, tokens before position 0
+ * and pages outside the table or the pool are skipped. */
+delta_status delta_kv_write_q8(const delta_desc* desc, const delta_page_table* pt, const int32_t* token_indptr,
+                               int32_t max_tokens, const void* k, const void* v, int64_t row_stride,
+                               const delta_q8_cache* cache, void* stream);
+
+/* Read tokens back in desc's dtype: row token_indptr[b] + i of k_out and v_out
+ * ([tokens][num_kv_heads][head_dim]) receives position token_start[b] + i of sequence b, i <
+ * token_indptr[b+1] - token_indptr[b] (token_start [batch] device, or NULL: the last tokens of each
+ * sequence, as delta_kv_write_q8 takes them).  max_tokens as there.  Positions outside 0..kv_len[b]-1 and
+ * pages outside the table or the pool leave their rows as they were. */
+delta_status delta_kv_read_q8(const delta_desc* desc, const delta_page_table* pt, const int32_t* token_indptr,
+                              int32_t max_tokens, const int32_t* token_start, const delta_q8_cache* cache,
+                              void* k_out, void* v_out, void* stream);
+
+/* Workspace of the attention calls below (delta_workspace_init it once, as delta_workspace_size's).
+ * reduce: DELTA_HEAD_SUM, or DELTA_HEAD_MAX for a delta_select_attn_q8 that scores with it. */
+size_t delta_workspace_size_q8(const delta_desc* desc, int32_t batch, int32_t max_pages_per_seq, int32_t reduce);
+
+/* The attention calls over the 8-bit cache: the same meaning, outputs and errors as their namesakes, with
+ * K and V the values the cache stands for.  q and o are in desc's dtype (bf16 or fp32). */
+delta_status delta_full_attn_q8(const delta_desc* desc, const delta_page_table* pt, const void* q,
+                                const delta_q8_cache* cache, void* o, void* workspace, size_t ws_bytes, void* stream);
+delta_status delta_select_attn_q8(const delta_desc* desc, const delta_page_table* pt, const delta_select_params* sp,
+                                  const void* q, const delta_q8_cache* cache, void* o, int32_t* sel_cnt,
+                                  int32_t* sel_pages, int32_t sel_stride, float* page_scores, void* workspace,
+                                  size_t ws_bytes, void* stream);
+delta_status delta_sparse_attn_q8(const delta_desc* desc, const delta_page_table* pt, const int32_t* sel_cnt,
+                                  const int32_t* sel_pages, int32_t sel_stride, const void* q,
+                                  const delta_q8_cache* cache, void* o, void* workspace, size_t ws_bytes,
+                                  void* stream);
+delta_status delta_sparse_attn_settled_q8(const delta_desc* desc, const delta_page_table* pt, const int32_t* sel_cnt,
+                                          const int32_t* sel_pages, int32_t sel_stride, const void* q,
+                                          const delta_q8_cache* cache, void* o, void* workspace, size_t ws_bytes,
+                                          void* stream);
+delta_status delta_window_attn_q8(const delta_desc* desc, const delta_page_table* pt, int32_t window_tokens,
+                                  int32_t sink_tokens, const void* q, const delta_q8_cache* cache, void* o,
+                                  void* workspace, size_t ws_bytes, void* stream);
 
 /* Delta-layer calibration metric: shift_out[b] = 1 - cos(scores_a[b], scores_b[b]) over the
  * pages j < ceil(kv_len[b]/page_size) of two layers' page scores (the page_scores outputs of

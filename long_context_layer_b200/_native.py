@@ -22,6 +22,9 @@ lib = ctypes.CDLL(LIB_PATH)
 DELTA_OK, DELTA_ERR_INVALID_ARG, DELTA_ERR_UNSUPPORTED, DELTA_ERR_WORKSPACE, DELTA_ERR_CUDA, DELTA_ERR_BOUNDS = range(6)
 DELTA_F32, DELTA_BF16 = 0, 1
 DELTA_HEAD_SUM, DELTA_HEAD_MAX = 0, 1
+DELTA_E4M3, DELTA_INT8 = 0, 1
+DELTA_ROPE_HALF, DELTA_ROPE_INTERLEAVED = 0, 1
+DELTA_ROPE_PLAIN, DELTA_ROPE_LINEAR, DELTA_ROPE_BANDS = 0, 1, 2
 
 EXPORTED = [
     "delta_workspace_size", "delta_workspace_size_reduce", "delta_workspace_init", "delta_sel_capacity", "delta_kv_append",
@@ -30,6 +33,10 @@ EXPORTED = [
     "delta_sparse_attn_settled",
     "delta_layer_shift", "delta_choose_layers", "delta_read_device_error",
     "delta_status_string",
+    "delta_window_attn", "delta_rope_table", "delta_rope",
+    "delta_kv_append_q8", "delta_kv_append_layers_q8", "delta_kv_write_q8", "delta_kv_read_q8",
+    "delta_workspace_size_q8", "delta_full_attn_q8", "delta_select_attn_q8", "delta_sparse_attn_q8",
+    "delta_sparse_attn_settled_q8", "delta_window_attn_q8",
 ]
 
 
@@ -49,6 +56,24 @@ class DeltaPageTable(ctypes.Structure):
 class DeltaSelectParams(ctypes.Structure):
     _fields_ = [("budget_pages", ctypes.c_int32), ("sink_tokens", ctypes.c_int32),
                 ("recency_tokens", ctypes.c_int32), ("reduce", ctypes.c_int32)]
+
+
+class DeltaRopeParams(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double), ("low_turns", ctypes.c_double),
+                ("high_turns", ctypes.c_double)]
+
+
+class DeltaRope(ctypes.Structure):
+    """delta_rope_plan"""
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("positions", ctypes.c_void_p), ("num_positions", ctypes.c_int32),
+                ("offset", ctypes.c_int32)]
+
+
+class DeltaQ8Cache(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32)]
 
 
 _vp, _sz, _i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
@@ -82,6 +107,25 @@ lib.delta_layer_shift.restype = _i32
 lib.delta_choose_layers.argtypes = [ctypes.POINTER(ctypes.c_float), _i32, _i32, _i32, _i32,
                                     ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
 lib.delta_choose_layers.restype = _i32
+_i64, _Q8 = ctypes.c_int64, ctypes.POINTER(DeltaQ8Cache)
+for _name, _args in {
+    "delta_window_attn": [_D, _PT, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "delta_rope_table": [ctypes.POINTER(DeltaRopeParams), ctypes.POINTER(ctypes.c_double)],
+    "delta_rope": [_D, ctypes.POINTER(DeltaRope), _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp],
+    "delta_kv_append_q8": [_D, _PT, _vp, _vp, _Q8, _vp],
+    "delta_kv_append_layers_q8": [_D, _PT, _i32, _vpp, _vpp, _Q8, _vp],
+    "delta_kv_write_q8": [_D, _PT, _vp, _i32, _vp, _vp, _i64, _Q8, _vp],
+    "delta_kv_read_q8": [_D, _PT, _vp, _i32, _vp, _Q8, _vp, _vp, _vp],
+    "delta_full_attn_q8": [_D, _PT, _vp, _Q8, _vp, _vp, _sz, _vp],
+    "delta_select_attn_q8": [_D, _PT, _SP, _vp, _Q8, _vp, _vp, _vp, _i32, _vp, _vp, _sz, _vp],
+    "delta_sparse_attn_q8": [_D, _PT, _vp, _vp, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
+    "delta_sparse_attn_settled_q8": [_D, _PT, _vp, _vp, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
+    "delta_window_attn_q8": [_D, _PT, _i32, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
+}.items():
+    getattr(lib, _name).argtypes = _args
+    getattr(lib, _name).restype = _i32
+lib.delta_workspace_size_q8.argtypes = [_D, _i32, _i32, _i32]
+lib.delta_workspace_size_q8.restype = _sz
 lib.delta_read_device_error.argtypes = [_vp, ctypes.POINTER(_i32), _vp]
 lib.delta_read_device_error.restype = _i32
 lib.delta_status_string.argtypes = [_i32]
@@ -203,3 +247,94 @@ def read_device_error(workspace, stream: int = 0) -> tuple:
     flags = _i32(0)
     s = lib.delta_read_device_error(ptr(workspace), ctypes.byref(flags), stream)
     return s, flags.value
+
+
+# ------------------------------------------------------------------ window layers
+def window_attn(desc, pt, window_tokens: int, sink_tokens: int, q, k_pool, v_pool, o, workspace, ws_bytes: int,
+                stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_window_attn(ctypes.byref(desc), ctypes.byref(pt), window_tokens, sink_tokens, ptr(q), ptr(k_pool),
+                              ptr(v_pool), ptr(o), ptr(workspace), ws_bytes, stream)
+    return _check(s, "delta_window_attn") if check else s
+
+
+# ------------------------------------------------------------------ rotary positions
+def rope_table(params: DeltaRopeParams) -> list:
+    """delta_rope_table: turns per token of each pair (host doubles; copy them to the device once)."""
+    out = (ctypes.c_double * max(params.rotary_dim // 2, 1))()
+    _check(lib.delta_rope_table(ctypes.byref(params), out), "delta_rope_table")
+    return list(out)
+
+
+def rope(desc, plan: DeltaRope, rows: int, q, q_out, k, k_out, q_stride: int = 0, q_out_stride: int = 0,
+         k_stride: int = 0, k_out_stride: int = 0, stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_rope(ctypes.byref(desc), ctypes.byref(plan), rows, ptr(q), q_stride, ptr(q_out), q_out_stride, ptr(k),
+                       k_stride, ptr(k_out), k_out_stride, stream)
+    return _check(s, "delta_rope") if check else s
+
+
+# ------------------------------------------------------------------ the cache held in 8 bits
+def workspace_size_q8(desc, batch: int, max_pages_per_seq: int, reduce: int = DELTA_HEAD_SUM) -> int:
+    return lib.delta_workspace_size_q8(ctypes.byref(desc), batch, max_pages_per_seq, reduce)
+
+
+def kv_append_q8(desc, pt, k_new, v_new, cache: DeltaQ8Cache, stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_kv_append_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(k_new), ptr(v_new), ctypes.byref(cache), stream)
+    return _check(s, "delta_kv_append_q8") if check else s
+
+
+def kv_append_layers_q8(desc, pt, k_new, v_new, caches, stream: int = 0, check: bool = True) -> int:
+    """k_new, v_new: one tensor or pointer per layer; caches: one DeltaQ8Cache per layer."""
+    n = len(caches)
+    s = lib.delta_kv_append_layers_q8(ctypes.byref(desc), ctypes.byref(pt), n, _ptr_array([k_new[l] for l in range(n)]),
+                                      _ptr_array([v_new[l] for l in range(n)]), (DeltaQ8Cache * n)(*caches), stream)
+    return _check(s, "delta_kv_append_layers_q8") if check else s
+
+
+def kv_write_q8(desc, pt, token_indptr, max_tokens: int, k, v, cache: DeltaQ8Cache, row_stride: int = 0,
+                stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_kv_write_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(token_indptr), max_tokens, ptr(k), ptr(v),
+                              row_stride, ctypes.byref(cache), stream)
+    return _check(s, "delta_kv_write_q8") if check else s
+
+
+def kv_read_q8(desc, pt, token_indptr, max_tokens: int, token_start, cache: DeltaQ8Cache, k_out, v_out,
+               stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_kv_read_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(token_indptr), max_tokens, ptr(token_start),
+                             ctypes.byref(cache), ptr(k_out), ptr(v_out), stream)
+    return _check(s, "delta_kv_read_q8") if check else s
+
+
+def full_attn_q8(desc, pt, q, cache: DeltaQ8Cache, o, workspace, ws_bytes: int, stream: int = 0,
+                 check: bool = True) -> int:
+    s = lib.delta_full_attn_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(q), ctypes.byref(cache), ptr(o), ptr(workspace),
+                               ws_bytes, stream)
+    return _check(s, "delta_full_attn_q8") if check else s
+
+
+def select_attn_q8(desc, pt, sp, q, cache: DeltaQ8Cache, o, sel_cnt, sel_pages, sel_stride: int, page_scores, workspace,
+                   ws_bytes: int, stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_select_attn_q8(ctypes.byref(desc), ctypes.byref(pt), ctypes.byref(sp), ptr(q), ctypes.byref(cache),
+                                 ptr(o), ptr(sel_cnt), ptr(sel_pages), sel_stride, ptr(page_scores), ptr(workspace),
+                                 ws_bytes, stream)
+    return _check(s, "delta_select_attn_q8") if check else s
+
+
+def sparse_attn_q8(desc, pt, sel_cnt, sel_pages, sel_stride: int, q, cache: DeltaQ8Cache, o, workspace, ws_bytes: int,
+                   stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_sparse_attn_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(sel_cnt), ptr(sel_pages), sel_stride, ptr(q),
+                                 ctypes.byref(cache), ptr(o), ptr(workspace), ws_bytes, stream)
+    return _check(s, "delta_sparse_attn_q8") if check else s
+
+
+def sparse_attn_settled_q8(desc, pt, sel_cnt, sel_pages, sel_stride: int, q, cache: DeltaQ8Cache, o, workspace,
+                           ws_bytes: int, stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_sparse_attn_settled_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(sel_cnt), ptr(sel_pages), sel_stride,
+                                         ptr(q), ctypes.byref(cache), ptr(o), ptr(workspace), ws_bytes, stream)
+    return _check(s, "delta_sparse_attn_settled_q8") if check else s
+
+
+def window_attn_q8(desc, pt, window_tokens: int, sink_tokens: int, q, cache: DeltaQ8Cache, o, workspace, ws_bytes: int,
+                   stream: int = 0, check: bool = True) -> int:
+    s = lib.delta_window_attn_q8(ctypes.byref(desc), ctypes.byref(pt), window_tokens, sink_tokens, ptr(q),
+                                 ctypes.byref(cache), ptr(o), ptr(workspace), ws_bytes, stream)
+    return _check(s, "delta_window_attn_q8") if check else s

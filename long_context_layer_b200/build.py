@@ -10,20 +10,25 @@ synth/libsynth_host.so (the same generator on the host, for fast oracle inputs).
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared"]
+COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
 
+CSRC = os.path.join(ROOT, "long_context_layer_b200", "csrc")
+# (sources, library, extra flags); the sources of one library compile side by side
 TARGETS = [
-    (os.path.join(ROOT, "long_context_layer_b200", "csrc", "delta_attn.cu"),
+    ([os.path.join(CSRC, f) for f in ("delta_attn.cu", "window_attn.cu", "attn_q8.cu", "attn_q8_e4m3.cu",
+                                      "attn_q8_int8.cu", "cache_q8.cu", "rope.cu")],
      os.path.join(ROOT, "long_context_layer_b200", "libdelta_attn.so"),
      ["-I" + os.path.join(ROOT, "include")]),
-    (os.path.join(ROOT, "synth", "csrc", "synth_fill.cu"),
+    ([os.path.join(ROOT, "synth", "csrc", "synth_fill.cu")],
      os.path.join(ROOT, "synth", "libsynth_fill.so"), []),
 ]
 # host (CPU) libraries built with gcc: the input generator's host copy
@@ -41,16 +46,21 @@ def nvcc() -> str:
 
 def build(force: bool = False, verbose: bool = False) -> list:
     built = []
-    for src, out, extra in TARGETS:
-        csrc = os.path.dirname(src)
+    for srcs, out, extra in TARGETS:
+        csrc = os.path.dirname(srcs[0])
         deps = [os.path.join(csrc, f) for f in os.listdir(csrc) if f.endswith((".cu", ".cuh", ".h"))]
         deps += [os.path.join(ROOT, "include", f) for f in os.listdir(os.path.join(ROOT, "include"))]
         if not force and os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(d) for d in deps):
             continue
-        cmd = [nvcc()] + ARCH + COMMON + extra + [src, "-o", out]
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        subprocess.run(cmd, check=True)
+        with tempfile.TemporaryDirectory() as tmp:
+            objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in srcs]
+            cmds = [[nvcc()] + ARCH + COMMON + extra + ["-c", src, "-o", obj] for src, obj in zip(srcs, objs)]
+            link = [nvcc()] + ARCH + ["-shared"] + objs + ["-o", out]
+            if verbose:
+                print("\n".join(" ".join(c) for c in cmds + [link]), file=sys.stderr)
+            with concurrent.futures.ThreadPoolExecutor(os.cpu_count()) as pool:
+                list(pool.map(lambda c: subprocess.run(c, check=True), cmds))
+            subprocess.run(link, check=True)
         built.append(out)
     for src, out in HOST_TARGETS:
         if not force and os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(src):

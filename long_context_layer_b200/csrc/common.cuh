@@ -23,7 +23,7 @@ constexpr int kMaxSplits = 512;   // the merge stages G*S*12 bytes of split weig
 constexpr uint32_t kWaitLimit = 1u << 24;   // try_wait polls before a stage wait gives up
 
 enum : int { kErrPage = 1, kErrLen = 2, kErrSel = 4, kErrTimeout = 8 };
-enum : int { kModeFull = 0, kModeDelta = 1, kModeSparse = 2 };
+enum : int { kModeFull = 0, kModeDelta = 1, kModeSparse = 2, kModeWindow = 3 };
 
 // ------------------------------------------------------------------ PTX helpers
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -216,6 +216,9 @@ struct DecodeParams {
                                      // KV heads by integer atomics; zero between launches
     uint32_t* keys;           // [B][max_pages] order keys of the page scores (when shared memory is short)
     int* seq_tickets;         // [B] units of a sequence that finished, zero between launches
+    int32_t window, sink;     // window layers: tokens t < sink or t >= kv_len - window are visible
+    const float* k_scale;     // 8-bit pools: [pages][Hkv] block scales, else null
+    const float* v_scale;
 };
 
 
@@ -241,11 +244,17 @@ struct SeqExtent {
     int N;                  // pages
     int pbeg;               // first entry of the sequence in page_indices
     int count;              // items to attend: N, or the selection length
+    int head, skip;         // window layers: items from `head` on are `skip` pages further (else unset)
+    int from;               // window layers: the window's first token
 };
 
+// Window layers: item i of the page list, which is the pages overlapping the first `sink` tokens, then
+// those overlapping the last `window`.
+__device__ __forceinline__ int window_page(const SeqExtent& ex, int i) { return i < ex.head ? i : i + ex.skip; }
+
 // QUIET: a speculative lookup (before the wait, for an L2 prefetch only) that raises no flags.
-// W: warps of the CTA (warp w streams items i0 + w, i0 + w + W, ...).
-template <bool QUIET = false, int W = kWarps, typename P>
+// W: warps of the CTA (warp w streams items i0 + w, i0 + w + W, ...).  WIN: window layers.
+template <bool QUIET = false, int W = kWarps, bool WIN = false, typename P>
 __device__ __forceinline__ void fetch_pages(const P& p, const SeqExtent& ex, int b, int i0, int warp, int nk, int kbase,
                                             int lane, int& lp, int& ph) {
     const int k = kbase + lane;
@@ -254,7 +263,8 @@ __device__ __forceinline__ void fetch_pages(const P& p, const SeqExtent& ex, int
     if (k >= nk) return;
     const int i = i0 + warp + k * W;
     // the selection is read from L2 (another kernel of the step wrote it; no stale L1 line)
-    lp = (p.mode == kModeSparse) ? __ldcg(p.sel_pages + size_t(b) * p.sel_stride + i) : i;
+    if constexpr (WIN) lp = window_page(ex, i);
+    else lp = (p.mode == kModeSparse) ? __ldcg(p.sel_pages + size_t(b) * p.sel_stride + i) : i;
     if (lp < 0 || lp >= ex.N) {
         if (!QUIET) atomicOr(p.err, kErrSel);
         lp = -1;
@@ -268,23 +278,23 @@ __device__ __forceinline__ void fetch_pages(const P& p, const SeqExtent& ex, int
     ph = int(x);
 }
 
-template <int W = kWarps, typename P>
+template <int W = kWarps, bool WIN = false, typename P>
 __device__ __forceinline__ void pages_init(WarpPages& w, const P& p, const SeqExtent& ex, int b, int i0, int warp,
                                            int nk, int lane) {
     w.cur = 0;
-    fetch_pages<false, W>(p, ex, b, i0, warp, nk, 0, lane, w.lp_a, w.ph_a);
-    fetch_pages<false, W>(p, ex, b, i0, warp, nk, 32, lane, w.lp_b, w.ph_b);
+    fetch_pages<false, W, WIN>(p, ex, b, i0, warp, nk, 0, lane, w.lp_a, w.ph_a);
+    fetch_pages<false, W, WIN>(p, ex, b, i0, warp, nk, 32, lane, w.lp_b, w.ph_b);
 }
 
 // Called by all lanes at the top of iteration k (uniform).
-template <int W = kWarps, typename P>
+template <int W = kWarps, bool WIN = false, typename P>
 __device__ __forceinline__ void pages_advance(WarpPages& w, const P& p, const SeqExtent& ex, int b, int i0, int warp,
                                               int nk, int lane, int k) {
     if (k > 0 && (k & 31) == 0) {
         w.cur = k >> 5;
         w.lp_a = w.lp_b;
         w.ph_a = w.ph_b;
-        fetch_pages<false, W>(p, ex, b, i0, warp, nk, (w.cur + 1) * 32, lane, w.lp_b, w.ph_b);
+        fetch_pages<false, W, WIN>(p, ex, b, i0, warp, nk, (w.cur + 1) * 32, lane, w.lp_b, w.ph_b);
     }
 }
 
@@ -325,6 +335,25 @@ __device__ __forceinline__ void seq_count(const P& p, int b, SeqExtent& ex) {
         if (threadIdx.x == 0) atomicOr(p.err, kErrSel);
         ex.count = min(max(scnt, 0), cap);
     }
+}
+
+// Window layers: the page list of sequence b.  Every listed page holds a visible token: the sinks' pages
+// start below min(sink, n), the window's end at or past its first token (a window of 0 lists none).
+template <typename P>
+__device__ __forceinline__ void seq_window(const P& p, SeqExtent& ex) {
+    const int sink = min(p.sink, ex.n);
+    ex.from = ex.n - min(p.window, ex.n);
+    ex.head = (sink + kPage - 1) / kPage;
+    const int first = p.window > 0 ? max(ex.from / kPage, ex.head) : ex.N;
+    ex.skip = first - ex.head;
+    ex.count = ex.head + max(ex.N - first, 0);
+    ex.count = min(ex.count, p.items_per_split * p.num_splits);
+}
+// Rows [lo, hi) of page lp that a window layer must not see (tokens between the sinks and the window).
+template <typename P>
+__device__ __forceinline__ void window_gap(const P& p, const SeqExtent& ex, int lp, int& lo, int& hi) {
+    lo = min(max(p.sink - lp * kPage, 0), kPage);
+    hi = min(max(ex.from - lp * kPage, 0), kPage);
 }
 
 // Floats of the dedicated receive area of the cluster merge (never aliased with pipeline stages,

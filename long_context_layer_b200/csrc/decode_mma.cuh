@@ -73,7 +73,9 @@ struct MmaSmem {
     static constexpr size_t kBytes = 1024 /* alignment slack */ + kMain + kBars + kRecv;
 };
 
-template <int D, int G, int STAGES, int WARPS>
+// WIN: window layers (tokens t < sink or t >= n - window), which also carry the probabilities as a sum of
+// two bf16 values, so that the output's error is its own rounding.
+template <int D, int G, int STAGES, int WARPS, bool WIN = false>
 __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeParams p,
                                                               const __grid_constant__ CUtensorMap tmap_k,
                                                               const __grid_constant__ CUtensorMap tmap_v) {
@@ -110,11 +112,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
     int i0 = 0, nk = 0;
     WarpPages pages;
     auto setup = [&]() {
-        seq_count(p, b, ex);
+        if constexpr (WIN) seq_window(p, ex);
+        else seq_count(p, b, ex);
         i0 = split * p.items_per_split;
         const int i1 = min(i0 + p.items_per_split, ex.count);
         nk = (i1 - i0 > warp) ? (i1 - i0 - warp + WARPS - 1) / WARPS : 0;   // pages of this warp
-        pages_init<WARPS>(pages, p, ex, b, i0, warp, nk, lane);
+        pages_init<WARPS, WIN>(pages, p, ex, b, i0, warp, nk, lane);
     };
     const uint64_t policy = evict_first_policy();
     // TMA of one page (K and V of KV head g) into stage k % STAGES; lane 0 only.
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
     uint32_t spec_used = 0;   // bit s: stage s spent its first phase on a discarded speculative load
     WarpPages spec;
     int nk_spec = 0;
-    if (p.mode != kModeSparse || p.settled) {
+    if (WIN || p.mode != kModeSparse || p.settled) {
         setup();   // a settled selection is final: read (and checked) now
     } else {
         const int cap = min(p.sel_stride, p.items_per_split * p.num_splits);
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
         spec.lp_b = spec.ph_b = -1;
     }
     {
-        const bool speculative = p.mode == kModeSparse && !p.settled;
+        const bool speculative = !WIN && p.mode == kModeSparse && !p.settled;
         const WarpPages& pre = speculative ? spec : pages;
         const int npre = min(STAGES, speculative ? nk_spec : nk);
         for (int k = 0; k < npre; ++k) {
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
         }
     }
 
-    if (p.mode == kModeSparse && !p.settled) {
+    if (!WIN && p.mode == kModeSparse && !p.settled) {
         // The selection's entries at the speculated positions are loaded together with its count
         // (one round trip); they are the real ones whenever the count is the speculated one.
         const int lp_real =
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
 
     // S^T (16 tokens x 8 heads) of the page in stage s; masked tokens get -inf.  Two accumulator
     // chains (even / odd k-steps) halve the dependent MMA chain.
-    auto qk_page = [&](int s, int tv, float (&sc)[4]) {
+    auto qk_page = [&](int s, int tv, int lp, float (&sc)[4]) {
         const uint32_t kbase = smem_addr(wst + size_t(s) * S::kPage);
         float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -274,7 +277,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
             else mma_bf16_16816(c0, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
         }
         // base-2 logits; tokens g4 and g4+8, heads 2*t4 and 2*t4+1
-        const bool ok0 = g4 < tv, ok1 = g4 + 8 < tv;
+        bool ok0 = g4 < tv, ok1 = g4 + 8 < tv;
+        if constexpr (WIN) {
+            int lo, hi;
+            window_gap(p, ex, lp, lo, hi);
+            ok0 = ok0 && (g4 < lo || g4 >= hi);
+            ok1 = ok1 && (g4 + 8 < lo || g4 + 8 >= hi);
+        }
         sc[0] = ok0 ? (c0[0] + c1[0]) * p.qscale : -INFINITY;
         sc[1] = ok0 ? (c0[1] + c1[1]) * p.qscale : -INFINITY;
         sc[2] = ok1 ? (c0[2] + c1[2]) * p.qscale : -INFINITY;
@@ -322,6 +331,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
         }
         __syncwarp();
     };
+    // window layers: the same for the V rows [lo, hi) between the sinks and the window
+    auto zero_gap = [&](int s, int lo, int hi) {
+        uint4* vz = reinterpret_cast<uint4*>(wst + size_t(s) * S::kPage + S::kBoxes * S::kBox);
+        const int per_box = (hi - lo) * 8;
+        for (int c = lane; c < S::kBoxes * per_box; c += 32) {
+            const int box = c / per_box, rem = c % per_box;
+            vz[box * (S::kBox / 16) + lo * 8 + rem] = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+    };
     // O^T += V^T . P^T for the page in stage s
     auto pv_page = [&](int s, uint32_t pb0, uint32_t pb1) {
         const uint32_t vbase = smem_addr(wst + size_t(s) * S::kPage) + S::kBoxes * S::kBox;
@@ -338,7 +357,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
     // Pages are taken two at a time: their QK products, one softmax update and their PV
     // products are independent chains the scheduler interleaves.
     for (int k = 0; k < nk; k += 2) {
-        pages_advance<WARPS>(pages, p, ex, b, i0, warp, nk, lane, k);
+        pages_advance<WARPS, WIN>(pages, p, ex, b, i0, warp, nk, lane, k);
         const bool two = k + 1 < nk;
         const int sA = k % STAGES, sB = (k + 1) % STAGES;
         if (!mbar_wait(&wbar[sA], parity(k)) || (two && !mbar_wait(&wbar[sB], parity(k + 1)))) {
@@ -355,11 +374,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
         const int tvB = vB ? min(kPage, ex.n - lpB * kPage) : 0;
         float scA[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float scB[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (vA) qk_page(sA, tvA, scA);
-        if (vB) qk_page(sB, tvB, scB);
+        if (vA) qk_page(sA, tvA, lpA, scA);
+        if (vB) qk_page(sB, tvB, lpB, scB);
         bool zeroed = false;
         if (vA || vB) {
-            if (p.logits != nullptr) {
+            if (!WIN && p.logits != nullptr) {
                 if (vA) store_logits(scA, lpA);
                 if (vB) store_logits(scB, lpB);
             }
@@ -376,7 +395,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
                                  exp2_approx(scA[3] - mn1)};
             const float pb[4] = {exp2_approx(scB[0] - mn0), exp2_approx(scB[1] - mn1), exp2_approx(scB[2] - mn0),
                                  exp2_approx(scB[3] - mn1)};
-            if (p.mode == kModeDelta) page_partials(pa, pb, mn0, mn1, al0, al1, vA, vB, lpA, lpB);
+            if (!WIN && p.mode == kModeDelta) page_partials(pa, pb, mn0, mn1, al0, al1, vA, vB, lpA, lpB);
             const uint32_t xa0 = pack_bf16(pa[0], pa[1]);
             const uint32_t xa1 = pack_bf16(pa[2], pa[3]);
             const uint32_t xb0 = pack_bf16(pb[0], pb[1]);
@@ -387,6 +406,21 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
             unpack_bf16x2(xb0, q0, q1);
             unpack_bf16x2(xb1, q2, q3);
             float rs0 = (p0 + p2) + (q0 + q2), rs1 = (p1 + p3) + (q1 + q3);
+            // window layers: what the rounding left over, rounded again (P = x + y to 2^-17)
+            uint32_t ya0 = 0, ya1 = 0, yb0 = 0, yb1 = 0;
+            if constexpr (WIN) {
+                ya0 = pack_bf16(pa[0] - p0, pa[1] - p1);
+                ya1 = pack_bf16(pa[2] - p2, pa[3] - p3);
+                yb0 = pack_bf16(pb[0] - q0, pb[1] - q1);
+                yb1 = pack_bf16(pb[2] - q2, pb[3] - q3);
+                float r0, r1, r2, r3, t0, t1, t2, t3;
+                unpack_bf16x2(ya0, r0, r1);
+                unpack_bf16x2(ya1, r2, r3);
+                unpack_bf16x2(yb0, t0, t1);
+                unpack_bf16x2(yb1, t2, t3);
+                rs0 += (r0 + r2) + (t0 + t2);
+                rs1 += (r1 + r3) + (t1 + t3);
+            }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 rs0 += __shfl_xor_sync(0xffffffffu, rs0, o);
@@ -405,6 +439,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
             }
             if (vA && tvA < kPage) { zero_tail(sA, tvA); zeroed = true; }
             if (vB && tvB < kPage) { zero_tail(sB, tvB); zeroed = true; }
+            if constexpr (WIN) {
+                int lo, hi;
+                window_gap(p, ex, lpA, lo, hi);
+                if (vA && lo < hi) { zero_gap(sA, lo, hi); zeroed = true; }
+                window_gap(p, ex, lpB, lo, hi);
+                if (vB && lo < hi) { zero_gap(sB, lo, hi); zeroed = true; }
+                if (vA) pv_page(sA, movmatrix_trans(ya0), movmatrix_trans(ya1));
+                if (vB) pv_page(sB, movmatrix_trans(yb0), movmatrix_trans(yb1));
+            }
             if (vA) pv_page(sA, movmatrix_trans(xa0), movmatrix_trans(xa1));
             if (vB) pv_page(sB, movmatrix_trans(xb0), movmatrix_trans(xb1));
         }
@@ -439,7 +482,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
         pml[(2 * t4) * 2 + 1] = l_run[0];
         pml[(2 * t4 + 1) * 2 + 0] = m_run[1];
         pml[(2 * t4 + 1) * 2 + 1] = l_run[1];
-        if (p.mode == kModeDelta) {
+        if (!WIN && p.mode == kModeDelta) {
             pdl[(2 * t4) * 2 + 0] = m_run[0];
             pdl[(2 * t4) * 2 + 1] = dl_run[0];
             pdl[(2 * t4 + 1) * 2 + 0] = m_run[1];
@@ -450,12 +493,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
     constexpr int kPart = STAGES * int(S::kPage) / 4;     // floats between two warps' records
     const float* mo0 = reinterpret_cast<const float*>(smem);
     float pre[2][G];   // delta-layers: this CTA's page terms, loaded before the merge
-    if (p.fuse_select) select_preload<WARPS * 32, G>(p, b, g, ex.N, pre);
+    if (!WIN && p.fuse_select) select_preload<WARPS * 32, G>(p, b, g, ex.N, pre);
     merge_epilogue<__nv_bfloat16, D, G, WARPS, WARPS * 32, kRow>(
         p, smem, mo0, mo0 + kMaxGroup * kRow, recv, b, g, kPart, kPart,
-        (p.mode == kModeDelta) ? mo0 + kMaxGroup * kRow + kMaxGroup * 2 : nullptr);
+        (!WIN && p.mode == kModeDelta) ? mo0 + kMaxGroup * kRow + kMaxGroup * 2 : nullptr);
     // delta-layers scoring with HEAD_SUM: page scores and the selection, in the stage area
-    if (p.fuse_select) select_tail<WARPS * 32, G, D>(p, smem, S::kStages, recv, b, g, ex.n, ex.N, pre);
+    if (!WIN && p.fuse_select) select_tail<WARPS * 32, G, D>(p, smem, S::kStages, recv, b, g, ex.n, ex.N, pre);
 }
 
 }  // namespace delta

@@ -19,7 +19,8 @@ struct DecodeSmem {
     static constexpr size_t kBytes = kMain + kBars + kPbuf + kAbuf + kRecv;
 };
 
-template <typename T, int D, int G, int STAGES>
+// WIN: window layers (tokens t < sink or t >= n - window).
+template <typename T, int D, int G, int STAGES, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams p) {
     using S = DecodeSmem<T, D, STAGES>;
     constexpr int DS = D / 16;          // dimensions per lane
@@ -56,11 +57,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
     int i0 = 0, nk = 0;
     WarpPages pages;
     auto setup = [&]() {
-        seq_count(p, b, ex);
+        if constexpr (WIN) seq_window(p, ex);
+        else seq_count(p, b, ex);
         i0 = split * p.items_per_split;
         const int i1 = min(i0 + p.items_per_split, ex.count);
         nk = (i1 - i0 > warp) ? (i1 - i0 - warp + kWarps - 1) / kWarps : 0;   // pages of this warp
-        pages_init(pages, p, ex, b, i0, warp, nk, lane);
+        pages_init<kWarps, WIN>(pages, p, ex, b, i0, warp, nk, lane);
     };
     const T* kpool = reinterpret_cast<const T*>(p.k_pool);
     const T* vpool = reinterpret_cast<const T*>(p.v_pool);
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
     // selection the caller states settled) know their pages, so the first stages' copies start
     // now, except the page holding the appended token, which the previous kernel may still write
     // (settled inputs: that one too); q goes to L2.
-    const bool known = p.mode != kModeSparse || p.settled;
+    const bool known = WIN || p.mode != kModeSparse || p.settled;
     uint32_t early = 0;   // bit k: page k's copy was issued before the wait
     if (known) {
         setup();
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
     int consumed = 0;
 
     for (int k = 0; k < nk; ++k) {
-        pages_advance(pages, p, ex, b, i0, warp, nk, lane, k);
+        pages_advance<kWarps, WIN>(pages, p, ex, b, i0, warp, nk, lane, k);
         const int s = k % STAGES;
         if (!mbar_wait(&wbar[s], (k / STAGES) & 1)) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
@@ -148,6 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
             const T* Ks = wst + size_t(s) * 2 * PE;
             const T* Vs = Ks + PE;
             const int tv = min(kPage, n - lp * kPage);     // valid tokens of this page
+            int lo = 0, hi = 0;                             // its hidden tokens [lo, hi)
+            if constexpr (WIN) window_gap(p, ex, lp, lo, hi);
             float sc[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -177,12 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
                 }
 #pragma unroll
                 for (int m = GP; m < 16; m <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
-                sc[j] = (t < tv) ? v[0] : -INFINITY;
+                sc[j] = (t < tv && (!WIN || t < lo || t >= hi)) ? v[0] : -INFINITY;
             }
             float mb = sc[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) mb = fmaxf(mb, sc[j]);
-            if (p.mode == kModeDelta) {
+            if (!WIN && p.mode == kModeDelta) {
                 const float mp = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
                 float e = 0.f;
 #pragma unroll
@@ -220,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
             const int jmax = min(8, tv - half * 8);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (j < jmax) {
-                    const int t = half * 8 + j;
+                const int t = half * 8 + j;
+                if (j < jmax && (!WIN || t < lo || t >= hi)) {
                     float vx[DS];
                     load_row<T, DS>(Vs + t * D + hl * DS, vx);
                     float pj[G];
@@ -257,10 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const DecodeParams 
     }
     __syncthreads();
     float pre[2][G];   // delta-layers: this CTA's page terms, loaded before the merge
-    if (p.fuse_select) select_preload<kThreads, G>(p, b, g, ex.N, pre);
+    if (!WIN && p.fuse_select) select_preload<kThreads, G>(p, b, g, ex.N, pre);
     merge_epilogue<T, D, G, kWarps * 2>(p, smem, mo, mml, recv, b, g, kMaxGroup * D, kMaxGroup * 2);
     // delta-layers scoring with HEAD_SUM: page scores and the selection, in the stage area
-    if (p.fuse_select) select_tail<kThreads, G, D>(p, smem, S::kMain, recv, b, g, ex.n, ex.N, pre);
+    if (!WIN && p.fuse_select) select_tail<kThreads, G, D>(p, smem, S::kMain, recv, b, g, ex.n, ex.N, pre);
 }
 
 }  // namespace delta
