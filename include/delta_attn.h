@@ -293,7 +293,7 @@ delta_status delta_rope(const delta_desc* desc, const delta_rope_plan* rope, int
  * scale; a value stands for payload * scale.  Scales are powers of two, 2^e with e the smallest
  * integer >= -100 such that the block's largest magnitude is at most QMAX * 2^e (QMAX 448 for e4m3, 127
  * for int8), so scaling is exact, a value is rounded once (to nearest even), and both formats read
- * back exactly in bf16 and fp32.
+ * back exactly in bf16 and fp32 (but for magnitudes that round up to 2^128: infinity there).
  * Tokens written into a block that already holds older tokens keep the larger of its scale and their
  * own; when the scale grows, the older values are rounded again to the new one.  Growth at least
  * doubles a step, so all roundings of a value together stay below one step of its block's scale.

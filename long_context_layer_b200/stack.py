@@ -7,6 +7,9 @@ every other layer runs sparse attention over the selection of the most recent
 delta-layer of the same decode step.  The step starts by appending the current
 token's k and v to every layer's paged pool in one launch (the cache is kept in full).
 
+Beyond that schedule a stack may hold window layers (the first tokens and the last ones), keep its
+cache in 8 bits with a scale per block (Q8Pools), and rotate q and the new k itself (Rotary).
+
 The runner only sequences C-ABI calls on one CUDA stream; it can capture the
 whole step in a CUDA graph so one replay launches every kernel of the step.
 """
@@ -16,12 +19,55 @@ import torch
 
 from . import _native as N
 
-FULL, DELTA, SPARSE = "full", "delta", "sparse"
+FULL, DELTA, SPARSE, WINDOW = "full", "delta", "sparse", "window"
+FORMATS = {"e4m3": N.DELTA_E4M3, "int8": N.DELTA_INT8}
 
 
 def layer_kinds(num_layers: int, delta_layers) -> list:
     first = min(delta_layers)
     return [DELTA if l in delta_layers else (FULL if l < first else SPARSE) for l in range(num_layers)]
+
+
+class Q8Pools:
+    """One layer's cache in 8 bits: payloads k, v [num_phys_pages, Hkv, 16, D] uint8 and block scales
+    k_scale, v_scale [num_phys_pages, Hkv] fp32 (format "e4m3" or "int8"); `c` is the descriptor the entry
+    points take (kv_write_q8 fills it from a prompt, kv_read_q8 reads it back)."""
+
+    def __init__(self, num_phys_pages: int, num_kv_heads: int, head_dim: int, format: str, device="cuda"):
+        if format not in FORMATS:
+            raise ValueError(f"format must be one of {sorted(FORMATS)}")
+        self.format = format
+        self.k = torch.zeros(num_phys_pages, num_kv_heads, 16, head_dim, dtype=torch.uint8, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.k_scale = torch.zeros(num_phys_pages, num_kv_heads, dtype=torch.float32, device=device)
+        self.v_scale = torch.zeros_like(self.k_scale)
+        self.c = N.DeltaQ8Cache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                                FORMATS[format])
+
+
+class Rotary:
+    """Rotary positions of a stack: the device table of delta_rope with its layout and magnitude.
+
+    scaling: "plain", "linear" (factor) or "bands" (factor, original_len, low_turns, high_turns), as
+    delta_rope_table defines them; layout: "half" or "interleaved"."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "plain",
+                 factor: float = 1.0, original_len: float = 0.0, low_turns: float = 0.0, high_turns: float = 0.0,
+                 magnitude: float = 1.0, device="cuda"):
+        layouts = {"half": N.DELTA_ROPE_HALF, "interleaved": N.DELTA_ROPE_INTERLEAVED}
+        kinds = {"plain": N.DELTA_ROPE_PLAIN, "linear": N.DELTA_ROPE_LINEAR, "bands": N.DELTA_ROPE_BANDS}
+        if layout not in layouts:
+            raise ValueError(f"layout must be one of {sorted(layouts)}")
+        if scaling not in kinds:
+            raise ValueError(f"scaling must be one of {sorted(kinds)}")
+        table = N.rope_table(N.DeltaRopeParams(rotary_dim, kinds[scaling], base, factor, original_len, low_turns, high_turns))
+        self.turns = torch.tensor(table, dtype=torch.float64, device=device)
+        self.rotary_dim, self.layout, self.magnitude = rotary_dim, layouts[layout], magnitude
+
+    def plan(self, positions: torch.Tensor, offset: int = 0) -> N.DeltaRope:
+        """delta_rope's plan for rows at positions[r % len] + offset (int32, on the device)."""
+        return N.DeltaRope(self.turns.data_ptr(), self.rotary_dim, self.layout, self.magnitude, positions.data_ptr(),
+                           positions.numel(), offset)
 
 
 class DeltaStack:
@@ -31,13 +77,28 @@ class DeltaStack:
       indptr [B+1], indices [nnz], kv_len [B]  int32 page table shared by all layers
       k_pools[l], v_pools[l]                   [num_phys_pages, Hkv, 16, D] per layer
       q [L, B, Hq, D], k_new / v_new [L, B, Hkv, D], out [L, B, Hq, D]
+
+    cache "e4m3" or "int8": the cache is held in 8 bits; k_pools is then a list of Q8Pools and v_pools None.
+    window_tokens, window_sinks: what the layers of kind "window" see.
+    rotary: q and k_new arrive unrotated and are rotated to each sequence's newest position first (the inputs
+    are left as they are).
     """
 
     def __init__(self, kinds, num_q_heads: int, num_kv_heads: int, head_dim: int, dtype: torch.dtype,
                  indptr: torch.Tensor, indices: torch.Tensor, kv_len: torch.Tensor, max_pages_per_seq: int,
                  num_phys_pages: int, budget_pages: int = 0, sink_tokens: int = 0, recency_tokens: int = 0,
-                 sm_scale: float = 0.0, keep_scores: bool = False, reduce: int = N.DELTA_HEAD_SUM):
+                 sm_scale: float = 0.0, keep_scores: bool = False, reduce: int = N.DELTA_HEAD_SUM,
+                 cache: str | None = None, window_tokens: int = 0, window_sinks: int = 0,
+                 rotary: Rotary | None = None):
         self.kinds = list(kinds)
+        unknown = set(self.kinds) - {FULL, DELTA, SPARSE, WINDOW}
+        if unknown:
+            raise ValueError(f"unknown layer kinds {sorted(unknown)}")
+        if cache is not None and cache not in FORMATS:
+            raise ValueError(f"cache must be None or one of {sorted(FORMATS)}")
+        if WINDOW in self.kinds and (window_tokens < 0 or window_sinks < 0 or window_tokens + window_sinks == 0):
+            raise ValueError("window layers need window_tokens and window_sinks >= 0, not both 0")
+        self.cache, self.window = cache, (window_tokens, window_sinks)
         self.device = indptr.device
         self.batch = int(kv_len.numel())
         self.dtype = dtype
@@ -50,7 +111,8 @@ class DeltaStack:
                                    max_pages_per_seq)
         self.sp = N.DeltaSelectParams(budget_pages, sink_tokens, recency_tokens, reduce)
         self.max_pages = max_pages_per_seq
-        self.ws_bytes = N.workspace_size_reduce(self.desc, self.batch, max_pages_per_seq, reduce)
+        size = N.workspace_size_reduce if cache is None else N.workspace_size_q8
+        self.ws_bytes = size(self.desc, self.batch, max_pages_per_seq, reduce)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         N.workspace_init(self.workspace, self.ws_bytes, torch.cuda.current_stream(self.device).cuda_stream)
         self.sel_stride = max(N.sel_capacity(self.sp), 1)
@@ -65,24 +127,56 @@ class DeltaStack:
             if not any(k == DELTA for k in self.kinds[:first_sparse]):
                 raise ValueError("a sparse layer needs an earlier delta-layer")
         self.graph = None
+        self.rope = None
+        if rotary is not None:
+            self.rotary, self.rope = rotary, rotary.plan(kv_len, -1)
+            L = len(self.kinds)
+            self.q_rot = torch.empty(L, self.batch, num_q_heads, head_dim, dtype=dtype, device=self.device)
+            self.k_rot = torch.empty(L, self.batch, num_kv_heads, head_dim, dtype=dtype, device=self.device)
 
     # ------------------------------------------------------------------ one step
     def launches_per_step(self, append: bool = True) -> int:
         # a delta-layer scoring with HEAD_SUM selects its pages inside its decode kernel; HEAD_MAX
         # adds a selection kernel
-        per = {FULL: 1, DELTA: 1 if self.sp.reduce == N.DELTA_HEAD_SUM else 2, SPARSE: 1}
-        return sum(per[k] for k in self.kinds) + (1 if append else 0)
+        per = {FULL: 1, DELTA: 1 if self.sp.reduce == N.DELTA_HEAD_SUM else 2, SPARSE: 1, WINDOW: 1}
+        return sum(per[k] for k in self.kinds) + (1 if append else 0) + (1 if self.rope is not None else 0)
+
+    def _rotate(self, q, k_new, a: int, b: int, st):
+        """q and k_new (None: q alone) of layers [a, b), rotated when the stack has rotary positions
+        (one launch)."""
+        if self.rope is None:
+            return q, k_new
+        k, k_out = (None, None) if k_new is None else (k_new[a:b], self.k_rot[a:b])
+        for x in (q[a:b], k):
+            if x is not None and not x.is_contiguous():
+                raise ValueError("q and k_new must be contiguous [layers, batch, heads, head_dim]")
+        N.rope(self.desc, self.rope, (b - a) * self.batch, q[a:b], self.q_rot[a:b], k, k_out, stream=st)
+        return self.q_rot, None if k_new is None else self.k_rot
+
+    def _append(self, k_new, v_new, k_pools, v_pools, a: int, b: int, st):
+        """The new token of layers [a, b) in one launch (layers do not read each other's pools)."""
+        if self.cache is None:
+            N.kv_append_layers(self.desc, self.pt, k_new[a:b], v_new[a:b], k_pools[a:b], v_pools[a:b], st)
+        else:
+            self._check_pools(k_pools[a:b])
+            N.kv_append_layers_q8(self.desc, self.pt, k_new[a:b], v_new[a:b], [x.c for x in k_pools[a:b]], st)
+
+    def _check_pools(self, pools):
+        for x in pools:
+            if not isinstance(x, Q8Pools) or x.format != self.cache or tuple(x.k.shape) != (
+                    self.desc.num_phys_pages, self.desc.num_kv_heads, 16, self.desc.head_dim):
+                raise ValueError(f"a stack with a {self.cache} cache takes Q8Pools of its format and shape")
 
     def step(self, q, k_new, v_new, k_pools, v_pools, out, append: bool = True, stream: int | None = None):
         st = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
-        d, pt = self.desc, self.pt
         cur = -1
-        if append:      # every layer's new token in one launch (layers do not read each other's pools)
-            N.kv_append_layers(d, pt, k_new, v_new, k_pools, v_pools, st)
+        q, k_new = self._rotate(q, k_new, 0, len(self.kinds), st)
+        if append:
+            self._append(k_new, v_new, k_pools, v_pools, 0, len(self.kinds), st)
         for l, kind in enumerate(self.kinds):
-            # a sparse layer after a sparse layer uses the settled entry: the selection and the
-            # appended tokens were final before the previous sparse layer began (it waited on the
-            # delta-layer that wrote the selection), so this layer may read them early
+            # a sparse layer after a sparse or window layer uses the settled entry: the selection and
+            # the appended tokens were final before the previous layer's kernel began its work (it
+            # waited on the delta-layer that wrote the selection), so this layer may read them early
             self._layer(l, kind, cur, q, k_pools, v_pools, out, st)
             if kind == DELTA:
                 cur = self.delta_layers.index(l)
@@ -126,11 +220,12 @@ class DeltaStack:
         cur, c0 = -1, 0
         for gi, (a, b) in enumerate(groups):
             main.wait_event(ready[gi])
+            q_use, k_use = self._rotate(q_dev, k_new_dev, a, b, st)
             if append:
-                N.kv_append_layers(self.desc, self.pt, k_new_dev[a:b], v_new_dev[a:b], k_pools[a:b], v_pools[a:b], st)
+                self._append(k_use, v_new_dev, k_pools, v_pools, a, b, st)
             for l in range(a, b):
                 kind = self.kinds[l]
-                self._layer(l, kind, cur, q_dev, k_pools, v_pools, out_dev, st)
+                self._layer(l, kind, cur, q_use, k_pools, v_pools, out_dev, st)
                 if kind == DELTA:
                     cur = self.delta_layers.index(l)
                 if l + 1 - c0 == per or l >= L - 2:
@@ -145,19 +240,27 @@ class DeltaStack:
 
     def _layer(self, l, kind, cur, q, k_pools, v_pools, out, st):
         d, pt, ws, wb = self.desc, self.pt, self.workspace, self.ws_bytes
+        # what the entry points of this cache take in the place of the pools
+        pools = (k_pools[l], v_pools[l]) if self.cache is None else (k_pools[l].c,)
+        q8 = self.cache is not None
         if kind == FULL:
-            N.full_attn(d, pt, q[l], k_pools[l], v_pools[l], out[l], ws, wb, st)
+            (N.full_attn_q8 if q8 else N.full_attn)(d, pt, q[l], *pools, out[l], ws, wb, st)
+        elif kind == WINDOW:
+            (N.window_attn_q8 if q8 else N.window_attn)(d, pt, *self.window, q[l], *pools, out[l], ws, wb, st)
         elif kind == DELTA:
             c = self.delta_layers.index(l)
             scores = self.page_scores[c] if self.page_scores is not None else None
-            N.select_attn(d, pt, self.sp, q[l], k_pools[l], v_pools[l], out[l], self.sel_cnt[c], self.sel_pages[c],
-                          self.sel_stride, scores, ws, wb, st)
-        elif l > 0 and self.kinds[l - 1] == SPARSE:
-            N.sparse_attn_settled(d, pt, self.sel_cnt[cur], self.sel_pages[cur], self.sel_stride, q[l], k_pools[l],
-                                  v_pools[l], out[l], ws, wb, st)
+            self._select(q[l], pools, out[l], self.sel_cnt[c], self.sel_pages[c], scores, st)
         else:
-            N.sparse_attn(d, pt, self.sel_cnt[cur], self.sel_pages[cur], self.sel_stride, q[l], k_pools[l],
-                          v_pools[l], out[l], ws, wb, st)
+            settled = l > 0 and self.kinds[l - 1] in (SPARSE, WINDOW)
+            fn = ((N.sparse_attn_settled_q8 if q8 else N.sparse_attn_settled) if settled
+                  else (N.sparse_attn_q8 if q8 else N.sparse_attn))
+            fn(d, pt, self.sel_cnt[cur], self.sel_pages[cur], self.sel_stride, q[l], *pools, out[l], ws, wb, st)
+
+    def _select(self, q, pools, out, sel_cnt, sel_pages, scores, st):
+        fn = N.select_attn if self.cache is None else N.select_attn_q8
+        fn(self.desc, self.pt, self.sp, q, *pools, out, sel_cnt, sel_pages, self.sel_stride, scores, self.workspace,
+           self.ws_bytes, st)
 
     # ------------------------------------------------------------------ CUDA graph
     def capture(self, *args, **kw) -> torch.cuda.CUDAGraph:
@@ -190,13 +293,14 @@ class DeltaStack:
         """
         st = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
         L = len(self.kinds)
+        q, _ = self._rotate(q, None, 0, L, st)
         scores = torch.zeros(L, self.batch, self.max_pages, dtype=torch.float32, device=self.device)
         shift = torch.zeros(L, self.batch, dtype=torch.float32, device=self.device)
         sel_cnt = torch.zeros(self.batch, dtype=torch.int32, device=self.device)
         sel_pages = torch.zeros(self.batch, self.sel_stride, dtype=torch.int32, device=self.device)
         for l in range(1, L):
-            N.select_attn(self.desc, self.pt, self.sp, q[l], k_pools[l], v_pools[l], out[l], sel_cnt, sel_pages,
-                          self.sel_stride, scores[l], self.workspace, self.ws_bytes, st)
+            pools = (k_pools[l], v_pools[l]) if self.cache is None else (k_pools[l].c,)
+            self._select(q[l], pools, out[l], sel_cnt, sel_pages, scores[l], st)
             if l >= 2:
                 N.layer_shift(self.pt, scores[l - 1], scores[l], shift[l], st)
         return shift
