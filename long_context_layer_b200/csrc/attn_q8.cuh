@@ -8,7 +8,13 @@ namespace delta {
 
 // bf16 queries: 8-warp CTAs, two an SM (kVarNarrow), or one 16-warp CTA an SM (kVarWide); the same pages in
 // flight.  fp32 queries carry every fragment twice and keep to 8 warps.
-constexpr int kQ8Warps = 8, kQ8WideWarps = 16, kQ8Stages = 3;
+#ifndef Q8_WIDE
+#define Q8_WIDE 3
+#endif
+#ifndef Q8_STAGES
+#define Q8_STAGES 3
+#endif
+constexpr int kQ8Warps = 8, kQ8WideWarps = 16, kQ8Stages = Q8_STAGES;
 
 struct Q8Kernel {
     const void* fn;

@@ -3,14 +3,18 @@
 //
 // Grid, clusters, page rings and the merge are those of the bf16 kernel (decode_mma.cuh); what differs is
 // what 8-bit blocks with one scale each allow and ask for.  Per page (16 tokens x D bytes of K and of V):
-//   S^T[16 x 8] = K8[16 x D] . Q^T[D x 8]   mma.m16n8k16 in fp16: an e4m3 or int8 value is exact in fp16, and
-//        one ldmatrix row of 16 bytes holds 16 dimensions, so a 4-byte register holds two 2-value fragments
-//        of one token: dimensions 4 t4 + {0, 1} and 4 t4 + {2, 3} of the chunk.  The product sums over
-//        dimensions, so their order is free as long as Q's fragments follow it.
+//   S^T[16 x 8] = K8[16 x D] . Q^T[D x 8]
+//        e4m3: mma.m16n8k16 in fp16, in which an e4m3 value is exact.  Q is scaled per head by a power of two so
+//        that its largest element is in [2^14, 2^15): a bf16 keeps its bits down to 2^-28 of the largest.  A
+//        4-byte register of an ldmatrix row holds two 2-value fragments of one token, dimensions 4 t4 + {0, 1}
+//        and 4 t4 + {2, 3} of a 16-byte chunk; the product sums over dimensions, so their order is free as long
+//        as Q's fragments follow it.  (The 8-bit mma.m16n8k32 over e4m3 operands is executed as two fp16
+//        products with conversions of both operands: 115 instead of 104 us for the delta-layer of 16 x 16k.)
+//        int8: the payload is an operand of mma.m16n8k32 over bytes, and a query is 16-bit fixed point, high
+//        bytes (signed) and low bytes (unsigned) on two integer accumulators: exact down to 2^-7 of the head's
+//        largest element, the others to 2^-15 of it.  No conversion of K (85 instead of 91 us for 4 x 64k).
+//        fp32 queries: the fp16 form with a query as the sum of two values (22 bits and the sign).
 //   s = S * (Q's factor per head) * (K's block scale): powers of two and the softmax scale, in fp32.
-//        Q is scaled per head by a power of two so that its largest element is in [2^14, 2^15): a bf16 value
-//        keeps all its bits in fp16 down to 2^-28 of the largest.  fp32 queries are a sum of two fp16 values
-//        (22 bits and the sign), which costs a second MMA.
 //   online softmax as in decode_mma.cuh, with p = 2^(s - m + 14) so that fp16 holds small probabilities
 //        (to 2^-39 of the largest; the offset cancels in o = acc / l), l summed from the rounded p that
 //        weigh V (fp32: p too is a sum of two fp16 values).
@@ -23,6 +27,8 @@
 
 #include "decode_mma.cuh"
 #include "q8.cuh"
+
+#include <type_traits>
 
 namespace delta {
 
@@ -38,13 +44,25 @@ struct Q8Smem {
     static constexpr size_t kBytes = 1024 /* alignment slack */ + kStages + kBars + kRecv;
 };
 
+// (Not volatile: the products depend on their registers alone, so independent chains interleave.)
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8s8_16832(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8u8_16832(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -52,27 +70,51 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
-// Bytes (i, j) of four payload bytes as two fp16 values.  e4m3: sign, 4 exponent bits and 3 mantissa bits
-// moved to fp16's places, which is the value times 2^-8 (subnormals too; kFold puts 2^8 back).  int8: the
-// byte with its sign bit flipped is value + 128, as fp16's 1024 + u, minus 1152.
+// Four payload bytes as fp16 pairs: near() gives bytes (0, 1) and (2, 3), apart() (0, 2) and (1, 3).
+// e4m3: the conversion instruction (after a byte permute for the pairs that are apart).  int8: a byte with its
+// sign bit flipped is value + 128; as the low byte of 0x6400 it is fp16's 1024 + (value + 128), minus 1152.
 template <int FMT>
-struct Half8 {
-    static constexpr float kFold = FMT == kE4M3 ? 256.f : 1.f;
-    static __device__ __forceinline__ uint32_t ready(uint32_t x) { return FMT == kE4M3 ? x : x ^ 0x80808080u; }
-    template <int I, int J>
-    static __device__ __forceinline__ uint32_t pair(uint32_t x) {
-        if constexpr (FMT == kE4M3) {
-            const uint32_t y = __byte_perm(x, 0u, 0x0404 | (I << 4) | (J << 12));    // bytes into the high halves
-            return (y & 0x80008000u) | ((y >> 1) & 0x3f803f80u);
-        } else {
-            const uint32_t y = __byte_perm(x, 0x64646464u, 0x4040 | I | (J << 8));
-            __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6480)));
-            return *reinterpret_cast<const uint32_t*>(&h);
-        }
+struct Half8;
+template <>
+struct Half8<kE4M3> {
+    static __device__ __forceinline__ uint32_t cvt(uint32_t two) {
+        uint32_t h;
+        asm("{ .reg .b16 l, u; mov.b32 {l, u}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(h) : "r"(two));
+        return h;
+    }
+    static __device__ __forceinline__ uint32_t cvt_high(uint32_t two) {
+        uint32_t h;
+        asm("{ .reg .b16 l, u; mov.b32 {l, u}, %1; cvt.rn.f16x2.e4m3x2 %0, u; }" : "=r"(h) : "r"(two));
+        return h;
+    }
+    static __device__ __forceinline__ void near(uint32_t x, uint32_t& lo, uint32_t& hi) {
+        lo = cvt(x);
+        hi = cvt_high(x);
+    }
+    static __device__ __forceinline__ void apart(uint32_t x, uint32_t& even, uint32_t& odd) {
+        near(__byte_perm(x, 0u, 0x3120), even, odd);
+    }
+};
+template <>
+struct Half8<kInt8> {
+    static __device__ __forceinline__ uint32_t less(uint32_t y) {
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ void near(uint32_t x, uint32_t& lo, uint32_t& hi) {
+        x ^= 0x80808080u;
+        lo = less(__byte_perm(x, 0x64646464u, 0x4140));
+        hi = less(__byte_perm(x, 0x64646464u, 0x4342));
+    }
+    static __device__ __forceinline__ void apart(uint32_t x, uint32_t& even, uint32_t& odd) {
+        x ^= 0x80808080u;
+        even = less(__byte_perm(x, 0x64646464u, 0x4240));
+        odd = less(__byte_perm(x, 0x64646464u, 0x4341));
     }
 };
 
-// Pages of a warp with their block scales, a lane holding one page of each of two chunks of 32.
+// Pages of a warp with their block scales, a lane holding one page of each of two chunks of 32 (a: the chunk
+// of the page in hand).  A page to be skipped has lp = ph = -1.
 struct Q8Pages {
     int lp_a, ph_a, lp_b, ph_b, cur;
     float ks_a, vs_a, ks_b, vs_b;
@@ -95,6 +137,7 @@ __device__ __forceinline__ void q8_lookup(const DecodeParams& p, const SeqExtent
     const int64_t x = p.indices[ex.pbeg + lp];
     if (x < 0 || x >= p.num_phys_pages) {
         atomicOr(p.err, kErrPage);
+        lp = -1;
         return;
     }
     ph = int(x);
@@ -116,6 +159,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     using S = Q8Smem<D, STAGES, WARPS>;
     using H = Half8<FMT>;
     constexpr bool kTwo = sizeof(T) == 4;      // fp32 queries and outputs: fp16 pairs
+    constexpr bool kHalf = kTwo || FMT == kE4M3;    // QK in fp16, else in 8-bit integers
     constexpr int KS = D / 16;                 // k-steps of the QK product = M-tiles of the PV product
     constexpr int CH = D / 32;                 // ldmatrix.x4 of a block
     constexpr float kShift = 14.f, kUnshift = 6.103515625e-05f;    // 2^14, 2^-14
@@ -173,22 +217,11 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
             q8_scales(p, g, pages.lp_b, pages.ph_b, -1, pages.ks_b, pages.vs_b);
         }
     };
-    auto page_at = [&](int k, int& lp, int& ph) {
-        const bool a = (k >> 5) == pages.cur;
-        lp = __shfl_sync(0xffffffffu, a ? pages.lp_a : pages.lp_b, k & 31);
-        ph = __shfl_sync(0xffffffffu, a ? pages.ph_a : pages.ph_b, k & 31);
+    auto phys_at = [&](int k) {
+        return __shfl_sync(0xffffffffu, (k >> 5) == pages.cur ? pages.ph_a : pages.ph_b, k & 31);
     };
-    auto scales_at = [&](int k, float& ks, float& vs) {
-        const bool a = (k >> 5) == pages.cur;
-        ks = __shfl_sync(0xffffffffu, a ? pages.ks_a : pages.ks_b, k & 31);
-        vs = __shfl_sync(0xffffffffu, a ? pages.vs_a : pages.vs_b, k & 31);
-    };
-    // all lanes call; lane 0 issues the copies of page k into stage k % STAGES
-    auto issue = [&](int k) {
-        int lp, ph;
-        page_at(k, lp, ph);
-        if (lane != 0) return;
-        const int s = k % STAGES;
+    // lane 0: the copies of a page into stage s
+    auto copy_page = [&](int ph, int s) {
         if (ph < 0) {
             mbar_arrive(&wbar[s]);   // completes the phase with no data; the page is skipped
             return;
@@ -198,6 +231,11 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         mbar_expect_tx(&wbar[s], S::kPage2);
         tma_load_2d(dst, &tmap_k, 0, y, &wbar[s], policy);
         tma_load_2d(dst + S::kBlock, &tmap_v, 0, y, &wbar[s], policy);
+    };
+    // all lanes call
+    auto issue = [&](int k, int s) {
+        const int ph = phys_at(k);
+        if (lane == 0) copy_page(ph, s);
     };
 
     if (threadIdx.x == 0)
@@ -209,10 +247,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     if (known) {
         setup(newest);
         for (int k = 0; k < min(STAGES, nk); ++k) {
-            int lp, ph;
-            page_at(k, lp, ph);
-            if (ph >= 0 && lp != newest) {
-                issue(k);
+            const int lp = __shfl_sync(0xffffffffu, pages.lp_a, k);
+            if (lp >= 0 && lp != newest) {
+                issue(k, k);
                 early |= 1u << k;
             }
         }
@@ -221,14 +258,15 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     pdl_trigger();
     if (!known) setup(-1);
     for (int k = 0; k < min(STAGES, nk); ++k)
-        if (!((early >> k) & 1u)) issue(k);
+        if (!((early >> k) & 1u)) issue(k, k);
     if (known && newest >= 0) {   // the newest page's scales, if this lane holds it
         if (pages.lp_a == newest) q8_scales(p, g, pages.lp_a, pages.ph_a, -1, pages.ks_a, pages.vs_a);
         if (pages.lp_b == newest) q8_scales(p, g, pages.lp_b, pages.ph_b, -1, pages.ks_b, pages.vs_b);
     }
 
-    // ---- Q^T fragments of head g4: dimensions 16 kk + 4 t4 + {0, 1} and {2, 3}
-    uint32_t qb[KS][2], ql[kTwo ? KS : 1][2];
+    // ---- Q^T fragments of head g4: dimensions 16 kk + 4 t4 + {0, 1, 2, 3} are this lane's
+    constexpr int kTop = 14;    // the largest element is scaled into [2^14, 2^15)
+    uint32_t qa[KS], qc[KS], qx[kTwo ? KS : 1], qy[kTwo ? KS : 1];
     float qf0, qf1;           // factors of this lane's logits (heads 2 t4, 2 t4 + 1)
     {
         float q[KS][4];
@@ -246,18 +284,27 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         // 2^x <= |q|max < 2^(x + 1), x at least -100; a head with a non-finite query gives NaN logits
         const int x = max(int(amax >> 23) - 127, -100);
         const bool fine = amax < 0x7f800000u;
-        const float up = fine ? __uint_as_float(uint32_t(14 - x + 127) << 23) : 0.f;
-        const float factor = fine ? p.qscale * H::kFold * __uint_as_float(uint32_t(x - 14 + 127) << 23) : __uint_as_float(0x7fc00000u);
+        const float up = fine ? __uint_as_float(uint32_t(kTop - x + 127) << 23) : 0.f;
+        const float factor = fine ? p.qscale * __uint_as_float(uint32_t(x - kTop + 127) << 23) : __uint_as_float(0x7fc00000u);
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) q[kk][j] = fine ? q[kk][j] * up : 0.f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                qb[kk][j] = pack_f16(q[kk][2 * j], q[kk][2 * j + 1]);
+            if constexpr (kHalf) {
+                qa[kk] = pack_f16(q[kk][0], q[kk][1]);
+                qc[kk] = pack_f16(q[kk][2], q[kk][3]);
                 if constexpr (kTwo) {
-                    const float2 r = unpack_f16(qb[kk][j]);
-                    ql[kk][j] = pack_f16(q[kk][2 * j] - r.x, q[kk][2 * j + 1] - r.y);
+                    const float2 ra = unpack_f16(qa[kk]), rc = unpack_f16(qc[kk]);
+                    qx[kk] = pack_f16(q[kk][0] - ra.x, q[kk][1] - ra.y);
+                    qy[kk] = pack_f16(q[kk][2] - rc.x, q[kk][3] - rc.y);
+                }
+            } else {
+                qa[kk] = qc[kk] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = __float2int_rn(q[kk][j]);       // within +-2^15 - 128
+                    qa[kk] |= (uint32_t(i >> 8) & 0xffu) << (8 * j);
+                    qc[kk] |= (uint32_t(i) & 0xffu) << (8 * j);
                 }
             }
         }
@@ -265,77 +312,97 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         qf1 = __shfl_sync(0xffffffffu, factor, 8 * t4 + 4);
     }
 
-    float m_run[2] = {-INFINITY, -INFINITY};   // heads 2*t4, 2*t4+1
+    // reference of the base-2 logits of heads 2 t4, 2 t4 + 1 (within 1 below their maximum or above it)
+    float m_run[2] = {-3.402823466e38f, -3.402823466e38f};
     float l_run[2] = {0.f, 0.f};               // this lane's tokens only; summed over the lanes at the end
     float dl_run[2] = {0.f, 0.f};              // delta-layers: the same over the unrounded terms
     float acc[KS][4];
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+    float vref = 1.175494351e-38f;             // unit of acc: the largest V scale so far
 
     // ldmatrix roles of this lane: matrix lj = (rows 8 (lj & 1) .. + 7, 16-byte chunk 2 c + (lj >> 1))
     const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
     const int sub = lane >> 4;
     const int swz = D == 128 ? (row & 7) : ((row >> 1) & 3);     // TMA swizzle: 128-byte or 64-byte rows
-    const uint32_t row_off = uint32_t(row) * D;
     bool failed = false;
     int consumed = 0;
 
-    // base-2 logits of the page in stage s: tokens g4, g4 + 8, heads 2 t4, 2 t4 + 1
-    auto qk_page = [&](int s, int lp, float ks, float (&sc)[4]) {
-        const uint32_t base = smem_addr(wst + size_t(s) * S::kPage2) + row_off;
-        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t off[CH];         // this lane's ldmatrix offsets in a block
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            uint32_t r0, r1, r2, r3;
-            ldmatrix_x4(base + (((2 * c + sub) ^ swz) << 4), r0, r1, r2, r3);
-            r0 = H::ready(r0);
-            r1 = H::ready(r1);
-            r2 = H::ready(r2);
-            r3 = H::ready(r3);
-            const uint32_t a0 = H::template pair<0, 1>(r0), a1 = H::template pair<0, 1>(r1);
-            const uint32_t a2 = H::template pair<2, 3>(r0), a3 = H::template pair<2, 3>(r1);
-            const uint32_t b0 = H::template pair<0, 1>(r2), b1 = H::template pair<0, 1>(r3);
-            const uint32_t b2 = H::template pair<2, 3>(r2), b3 = H::template pair<2, 3>(r3);
-            mma_f16_16816(c0, a0, a1, a2, a3, qb[2 * c][0], qb[2 * c][1]);
-            mma_f16_16816(c1, b0, b1, b2, b3, qb[2 * c + 1][0], qb[2 * c + 1][1]);
-            if constexpr (kTwo) {
-                mma_f16_16816(c0, a0, a1, a2, a3, ql[2 * c][0], ql[2 * c][1]);
-                mma_f16_16816(c1, b0, b1, b2, b3, ql[2 * c + 1][0], ql[2 * c + 1][1]);
-            }
+    for (int c = 0; c < CH; ++c) off[c] = uint32_t(row) * D + (((2 * c + sub) ^ swz) << 4);
+    const uint32_t st0 = smem_addr(wst);
+
+    // K . Q^T of 32 dimensions of the page in stage s.  c0 and c1: of the chunk's two halves (fp16), or the
+    // products with Q's high and low bytes.
+    using Sum = std::conditional_t<kHalf, float, int>;
+    auto qk_chunk = [&](int s, int c, Sum (&c0)[4], Sum (&c1)[4]) {
+        uint32_t r[4];
+        ldmatrix_x4(st0 + uint32_t(s) * S::kPage2 + off[c], r[0], r[1], r[2], r[3]);
+        if constexpr (kHalf) {
+            uint32_t a0, a1, a2, a3;
+            H::near(r[0], a0, a2);
+            H::near(r[1], a1, a3);
+            mma_f16_16816(c0, a0, a1, a2, a3, qa[2 * c], qc[2 * c]);
+            if constexpr (kTwo) mma_f16_16816(c0, a0, a1, a2, a3, qx[2 * c], qy[2 * c]);
+            H::near(r[2], a0, a2);
+            H::near(r[3], a1, a3);
+            mma_f16_16816(c1, a0, a1, a2, a3, qa[2 * c + 1], qc[2 * c + 1]);
+            if constexpr (kTwo) mma_f16_16816(c1, a0, a1, a2, a3, qx[2 * c + 1], qy[2 * c + 1]);
+        } else {
+            mma_s8s8_16832(c0, r, qa[2 * c], qa[2 * c + 1]);
+            mma_s8u8_16832(c1, r, qc[2 * c], qc[2 * c + 1]);
         }
-        const int t = lp * kPage + g4;
-        bool ok0 = t < ex.n, ok1 = t + 8 < ex.n;
-        if (p.mode == kModeWindow) {
-            ok0 = ok0 && (t < p.sink || t >= ex.from);
-            ok1 = ok1 && (t + 8 < p.sink || t + 8 >= ex.from);
-        }
-        sc[0] = ok0 ? (c0[0] + c1[0]) * qf0 * ks : -INFINITY;
-        sc[1] = ok0 ? (c0[1] + c1[1]) * qf1 * ks : -INFINITY;
-        sc[2] = ok1 ? (c0[2] + c1[2]) * qf0 * ks : -INFINITY;
-        sc[3] = ok1 ? (c0[3] + c1[3]) * qf1 * ks : -INFINITY;
     };
-    // delta-layers: a page's log2-sum-exp per head from the terms 2^(s - m + 14), as in decode_mma.cuh
+    auto sum_of = [](Sum high, Sum low) {
+        if constexpr (std::is_same_v<Sum, int>) return float(high * 256 + low);
+        else return high + low;
+    };
+    // base-2 logits of a page: tokens g4, g4 + 8, heads 2 t4, 2 t4 + 1
+    auto logits_of = [&](const Sum (&c0)[4], const Sum (&c1)[4], float ks, int lp, int s, float (&sc)[4]) {
+        const float f0 = qf0 * ks, f1 = qf1 * ks;
+        sc[0] = sum_of(c0[0], c1[0]) * f0;
+        sc[1] = sum_of(c0[1], c1[1]) * f1;
+        sc[2] = sum_of(c0[2], c1[2]) * f0;
+        sc[3] = sum_of(c0[3], c1[3]) * f1;
+        const int t0 = lp * kPage;
+        const bool whole = t0 + kPage <= ex.n && (p.mode != kModeWindow || t0 + kPage <= p.sink || t0 >= ex.from);
+        if (!whole) {      // the last page, and pages at the edge of the sinks or the window
+            const int t = t0 + g4;
+            bool ok0 = t < ex.n, ok1 = t + 8 < ex.n;
+            if (p.mode == kModeWindow) {
+                ok0 = ok0 && (t < p.sink || t >= ex.from);
+                ok1 = ok1 && (t + 8 < p.sink || t + 8 >= ex.from);
+            }
+            if (!ok0) sc[0] = sc[1] = -INFINITY;
+            if (!ok1) sc[2] = sc[3] = -INFINITY;
+            // slots past the end may hold e4m3's NaN: their V rows become zeros
+            const int tv = min(ex.n - t0, kPage);
+            uint4* vz = reinterpret_cast<uint4*>(wst + size_t(s) * S::kPage2 + S::kBlock);
+            for (int i = tv * (D / 16) + lane; i < kPage * (D / 16); i += 32) vz[i] = make_uint4(0, 0, 0, 0);
+            __syncwarp();
+            if (lane == 0) fence_proxy_async_smem();    // ahead of the copy that reuses the stage
+        }
+    };
+    // Delta-layers: a page's log2-sum-exp per head from the terms 2^(s - m + 14), summed over the g4 lanes.  The four
+    // sums of a lane (pages A and B, heads 2 t4 and 2 t4 + 1) are scattered as they are reduced, so each lane
+    // ends with one of them: page B where lane & 16, head 2 t4 + 1 where lane & 8.
+    const bool pick_b = lane & 16, pick_1 = lane & 8;
+    const int lse_head = 2 * t4 + (pick_1 ? 1 : 0);
+    float* lse_row = p.page_lse + (size_t(b) * Hq + h0 + (lse_head < G ? lse_head : 0)) * p.max_pages;
     auto page_partials = [&](const float (&pa)[4], const float (&pb)[4], float mn0, float mn1, float al0, float al1,
-                             bool vA, bool vB, int lpA, int lpB) {
-        float ea0 = pa[0] + pa[2], ea1 = pa[1] + pa[3], eb0 = pb[0] + pb[2], eb1 = pb[1] + pb[3];
+                             int lpA, int lpB) {
+        const float ea0 = pa[0] + pa[2], ea1 = pa[1] + pa[3], eb0 = pb[0] + pb[2], eb1 = pb[1] + pb[3];
         dl_run[0] = dl_run[0] * al0 + (ea0 + eb0);
         dl_run[1] = dl_run[1] * al1 + (ea1 + eb1);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            ea0 += __shfl_xor_sync(0xffffffffu, ea0, o);
-            ea1 += __shfl_xor_sync(0xffffffffu, ea1, o);
-            eb0 += __shfl_xor_sync(0xffffffffu, eb0, o);
-            eb1 += __shfl_xor_sync(0xffffffffu, eb1, o);
-        }
-        const int hA = 2 * t4, hB = 2 * t4 + 1;
-        if (g4 == 0) {
-            float* out = p.page_lse + (size_t(b) * Hq + h0) * p.max_pages;
-            const float u0 = mn0 - kShift, u1 = mn1 - kShift;
-            if (vA && hA < G) out[size_t(hA) * p.max_pages + lpA] = u0 + log2_approx(ea0);
-            if (vA && hB < G) out[size_t(hB) * p.max_pages + lpA] = u1 + log2_approx(ea1);
-            if (vB && hA < G) out[size_t(hA) * p.max_pages + lpB] = u0 + log2_approx(eb0);
-            if (vB && hB < G) out[size_t(hB) * p.max_pages + lpB] = u1 + log2_approx(eb1);
-        }
+        float e0 = pick_b ? eb0 : ea0, e1 = pick_b ? eb1 : ea1;
+        e0 += __shfl_xor_sync(0xffffffffu, pick_b ? ea0 : eb0, 16);
+        e1 += __shfl_xor_sync(0xffffffffu, pick_b ? ea1 : eb1, 16);
+        float e = pick_1 ? e1 : e0;
+        e += __shfl_xor_sync(0xffffffffu, pick_1 ? e0 : e1, 8);
+        e += __shfl_xor_sync(0xffffffffu, e, 4);
+        const int lp = pick_b ? lpB : lpA;
+        if ((lane & 4) == 0 && lp >= 0 && lse_head < G) lse_row[lp] = (pick_1 ? mn1 : mn0) - kShift + log2_approx(e);
     };
     auto store_logits = [&](const float (&sc)[4], int lp) {      // HEAD_MAX scoring
         float* lg = p.logits + (size_t(b) * Hq + h0) * (size_t(p.max_pages) * kPage) + size_t(lp) * kPage;
@@ -343,25 +410,39 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         if (2 * t4 < G) { lg[2 * t4 * hs + g4] = sc[0]; lg[2 * t4 * hs + g4 + 8] = sc[2]; }
         if (2 * t4 + 1 < G) { lg[(2 * t4 + 1) * hs + g4] = sc[1]; lg[(2 * t4 + 1) * hs + g4 + 8] = sc[3]; }
     };
-    // Tile pair c (dimensions 32 c .. 32 c + 31) of V^T . P^T of the page in stage s, added to d0 and d1.  Hidden
-    // tokens weigh exactly 0 and any payload byte is a finite fp16 value, so stale slots need no clearing.
+    // Tile pair c (dimensions 32 c .. 32 c + 31) of V^T . P^T of the page in stage s, added to d0 and d1.
     auto pv_tile = [&](int s, int c, const uint32_t (&pt)[kTwo ? 4 : 2], float (&d0)[4], float (&d1)[4]) {
-        const uint32_t base = smem_addr(wst + size_t(s) * S::kPage2) + S::kBlock + row_off;
-        uint32_t r0, r1, r2, r3;
-        ldmatrix_x4_trans(base + (((2 * c + sub) ^ swz) << 4), r0, r1, r2, r3);
-        r0 = H::ready(r0);
-        r1 = H::ready(r1);
-        r2 = H::ready(r2);
-        r3 = H::ready(r3);
-        const uint32_t a0 = H::template pair<0, 2>(r0), a1 = H::template pair<1, 3>(r0);
-        const uint32_t a2 = H::template pair<0, 2>(r1), a3 = H::template pair<1, 3>(r1);
-        const uint32_t b0 = H::template pair<0, 2>(r2), b1 = H::template pair<1, 3>(r2);
-        const uint32_t b2 = H::template pair<0, 2>(r3), b3 = H::template pair<1, 3>(r3);
+        uint32_t r0, r1, r2, r3, a0, a1, a2, a3;
+        ldmatrix_x4_trans(st0 + uint32_t(s) * S::kPage2 + S::kBlock + off[c], r0, r1, r2, r3);
+        H::apart(r0, a0, a1);
+        H::apart(r1, a2, a3);
         mma_f16_16816(d0, a0, a1, a2, a3, pt[0], pt[1]);
-        mma_f16_16816(d1, b0, b1, b2, b3, pt[0], pt[1]);
-        if constexpr (kTwo) {
-            mma_f16_16816(d0, a0, a1, a2, a3, pt[2], pt[3]);
-            mma_f16_16816(d1, b0, b1, b2, b3, pt[2], pt[3]);
+        if constexpr (kTwo) mma_f16_16816(d0, a0, a1, a2, a3, pt[2], pt[3]);
+        H::apart(r2, a0, a1);
+        H::apart(r3, a2, a3);
+        mma_f16_16816(d1, a0, a1, a2, a3, pt[0], pt[1]);
+        if constexpr (kTwo) mma_f16_16816(d1, a0, a1, a2, a3, pt[2], pt[3]);
+    };
+    // A page whose V scale is not the accumulators' unit (the largest scale so far).  Powers of two: exact.
+    auto pv_rescaled = [&](int s, const uint32_t (&pt)[kTwo ? 4 : 2], float vs) {
+        if (!(fabsf(vs) <= vref)) {      // a larger unit (or NaN)
+            const float r = vref / fabsf(vs);
+            vref = fabsf(vs);
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[mt][j] *= r;
+        }
+        const float w = vs / vref;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+            pv_tile(s, c, pt, d0, d1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[2 * c][j] = fmaf(d0[j], w, acc[2 * c][j]);
+                acc[2 * c + 1][j] = fmaf(d1[j], w, acc[2 * c + 1][j]);
+            }
         }
     };
     // the rounded probabilities of a page as P^T fragments; adds them to this lane's sums
@@ -382,97 +463,111 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         }
     };
 
+    // stages of the pages in hand and the parity of their phases (page k: stage k % STAGES, phase k / STAGES)
+    int sA = 0;
+    uint32_t parity = 0;
     for (int k = 0; k < nk; k += 2) {
         advance(k);
         const bool two = k + 1 < nk;
-        const int sA = k % STAGES, sB = (k + 1) % STAGES;
-        if (!mbar_wait(&wbar[sA], (k / STAGES) & 1) || (two && !mbar_wait(&wbar[sB], ((k + 1) / STAGES) & 1))) {
+        const int sB = sA + 1 == STAGES ? 0 : sA + 1;
+        const uint32_t parity_b = sB == 0 ? parity ^ 1u : parity;
+        if (!mbar_wait(&wbar[sA], parity) || (two && !mbar_wait(&wbar[sB], parity_b))) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
             failed = true;
             break;
         }
         consumed = k + (two ? 2 : 1);
-        int lpA, phA, lpB = -1, phB = -1;
-        float ksA, vsA, ksB = 0.f, vsB = 0.f;
-        page_at(k, lpA, phA);
-        scales_at(k, ksA, vsA);
-        if (two) {
-            page_at(k + 1, lpB, phB);
-            scales_at(k + 1, ksB, vsB);
-        }
-        const bool vA = phA >= 0, vB = phB >= 0;
-        float scA[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        float scB[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (vA) qk_page(sA, lpA, ksA, scA);
-        if (vB) qk_page(sB, lpB, ksB, scB);
+        const int src = k & 31;      // k is even: both pages are in chunk a
+        const int lpA = __shfl_sync(0xffffffffu, pages.lp_a, src);
+        const float ksA = __shfl_sync(0xffffffffu, pages.ks_a, src), vsA = __shfl_sync(0xffffffffu, pages.vs_a, src);
+        const int lpB = two ? __shfl_sync(0xffffffffu, pages.lp_a, src + 1) : -1;
+        const float ksB = __shfl_sync(0xffffffffu, pages.ks_a, src + 1), vsB = __shfl_sync(0xffffffffu, pages.vs_a, src + 1);
+        const bool vA = lpA >= 0, vB = lpB >= 0;
         if (vA || vB) {
+            // a page that is skipped, or missing behind the last, is stood in for by the other with weights of 0
+            const int pA = vA ? sA : sB, pB = vB ? sB : sA;
+            const float kA = vA ? ksA : ksB, kB = vB ? ksB : ksA, wA = vA ? vsA : vsB, wB = vB ? vsB : vsA;
+            float scA[4], scB[4];
+            {
+                Sum a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0}, b0[4] = {0, 0, 0, 0}, b1[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    qk_chunk(pA, c, a0, a1);
+                    qk_chunk(pB, c, b0, b1);
+                }
+                logits_of(a0, a1, kA, vA ? lpA : lpB, pA, scA);
+                logits_of(b0, b1, kB, vB ? lpB : lpA, pB, scB);
+            }
+            if (!vA) scA[0] = scA[1] = scA[2] = scA[3] = -INFINITY;
+            if (!vB) scB[0] = scB[1] = scB[2] = scB[3] = -INFINITY;
             if (p.logits != nullptr) {
                 if (vA) store_logits(scA, lpA);
                 if (vB) store_logits(scB, lpB);
             }
             float mx0 = fmaxf(fmaxf(scA[0], scA[2]), fmaxf(scB[0], scB[2]));
             float mx1 = fmaxf(fmaxf(scA[1], scA[3]), fmaxf(scB[1], scB[3]));
+            float al0 = 1.f, al1 = 1.f;
+            // The reference m need not be the maximum, only so near it that 2^(s - m + 14) fits fp16 (below 2^16):
+            // it moves when a logit passes it by more than 1, rarely after a few pages.  (NaN logits never do;
+            // their sums are NaN.)
+            if (__any_sync(0xffffffffu, mx0 > m_run[0] + 1.f || mx1 > m_run[1] + 1.f)) {
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                for (int o = 4; o < 32; o <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                }
+                const float m0 = fmaxf(m_run[0], mx0), m1 = fmaxf(m_run[1], mx1);
+                al0 = exp2_approx(m_run[0] - m0);
+                al1 = exp2_approx(m_run[1] - m1);
+                m_run[0] = m0;
+                m_run[1] = m1;
+                l_run[0] *= al0;
+                l_run[1] *= al1;
+#pragma unroll
+                for (int mt = 0; mt < KS; ++mt) {
+                    acc[mt][0] *= al0;
+                    acc[mt][1] *= al1;
+                    acc[mt][2] *= al0;
+                    acc[mt][3] *= al1;
+                }
             }
-            // the lowest finite value when every logit is NaN (fmaxf drops them): the sums then are NaN
-            const float mn0 = fmaxf(fmaxf(m_run[0], mx0), -3.402823466e38f);
-            const float mn1 = fmaxf(fmaxf(m_run[1], mx1), -3.402823466e38f);
-            const float al0 = exp2_approx(m_run[0] - mn0), al1 = exp2_approx(m_run[1] - mn1);
+            const float mn0 = m_run[0], mn1 = m_run[1];
             const float u0 = kShift - mn0, u1 = kShift - mn1;
             const float pa[4] = {exp2_approx(scA[0] + u0), exp2_approx(scA[1] + u1), exp2_approx(scA[2] + u0),
                                  exp2_approx(scA[3] + u1)};
             const float pb[4] = {exp2_approx(scB[0] + u0), exp2_approx(scB[1] + u1), exp2_approx(scB[2] + u0),
                                  exp2_approx(scB[3] + u1)};
-            if (p.mode == kModeDelta) page_partials(pa, pb, mn0, mn1, al0, al1, vA, vB, lpA, lpB);
+            if (p.mode == kModeDelta) page_partials(pa, pb, mn0, mn1, al0, al1, lpA, lpB);
             uint32_t ptA[kTwo ? 4 : 2], ptB[kTwo ? 4 : 2];
-            float s0 = 0.f, s1 = 0.f;
-            round_p(pa, ptA, s0, s1);
-            round_p(pb, ptB, s0, s1);
-            l_run[0] = l_run[0] * al0 + s0;
-            l_run[1] = l_run[1] * al1 + s1;
-            m_run[0] = mn0;
-            m_run[1] = mn1;
-            // The two pages' products share one accumulator when their V scales are equal (mostly: powers of
-            // two of similar blocks), else each is scaled by its own.
-            const float wA = vsA * (H::kFold * kUnshift), wB = vsB * (H::kFold * kUnshift);
-            const bool joint = vA && vB && vsA == vsB;
+            round_p(pa, ptA, l_run[0], l_run[1]);
+            round_p(pb, ptB, l_run[0], l_run[1]);
+            if (wA == vref && wB == vref) {     // mostly: powers of two of similar blocks
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-                float(&a0)[4] = acc[2 * c];
-                float(&a1)[4] = acc[2 * c + 1];
-                if (vA) pv_tile(sA, c, ptA, d0, d1);
-                if (joint) pv_tile(sB, c, ptB, d0, d1);
-                const float w = vA ? wA : 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float al = (j & 1) ? al1 : al0;
-                    a0[j] = fmaf(d0[j], w, a0[j] * al);
-                    a1[j] = fmaf(d1[j], w, a1[j] * al);
+                for (int c = 0; c < CH; ++c) {
+                    pv_tile(pA, c, ptA, acc[2 * c], acc[2 * c + 1]);
+                    pv_tile(pB, c, ptB, acc[2 * c], acc[2 * c + 1]);
                 }
-                if (vB && !joint) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d0[j] = d1[j] = 0.f;
-                    pv_tile(sB, c, ptB, d0, d1);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a0[j] = fmaf(d0[j], wB, a0[j]);
-                        a1[j] = fmaf(d1[j], wB, a1[j]);
-                    }
-                }
+            } else {
+                pv_rescaled(pA, ptA, wA);
+                pv_rescaled(pB, ptB, wB);
             }
         }
         __syncwarp();
-        if (k + STAGES < nk) issue(k + STAGES);
-        if (two && k + 1 + STAGES < nk) issue(k + 1 + STAGES);
+        if (k + STAGES < nk) {
+            const int ph0 = phys_at(k + STAGES), ph1 = phys_at(k + STAGES + 1);
+            if (lane == 0) {
+                copy_page(ph0, sA);
+                if (k + STAGES + 1 < nk) copy_page(ph1, sB);
+            }
+        }
+        sA = sB + 1 == STAGES ? 0 : sB + 1;
+        parity = sA == 0 ? parity_b ^ 1u : parity_b;
     }
     if (failed) {
         // drain this warp's copies still in flight (bounded) before shared memory is released
         for (int k = consumed + 1; k < min(consumed + STAGES, nk); ++k) mbar_wait(&wbar[k % STAGES], (k / STAGES) & 1);
     }
+    const float unit = vref * kUnshift;      // of the accumulators
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
 #pragma unroll
@@ -481,6 +576,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
             dl_run[j] += __shfl_xor_sync(0xffffffffu, dl_run[j], o);
         }
     }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (l_run[j] == 0.f) m_run[j] = -INFINITY;   // no token (a token at the reference weighs 2^13 or more)
 
     // ---- this warp's state into its own stage area, then the merge of the CTA's warps and of the splits
     __syncwarp();
@@ -491,8 +589,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) {
         const int d = mt * 16 + 2 * g4;
-        *reinterpret_cast<float2*>(po + (2 * t4) * kRow + d) = make_float2(acc[mt][0], acc[mt][2]);
-        *reinterpret_cast<float2*>(po + (2 * t4 + 1) * kRow + d) = make_float2(acc[mt][1], acc[mt][3]);
+        *reinterpret_cast<float2*>(po + (2 * t4) * kRow + d) = make_float2(acc[mt][0] * unit, acc[mt][2] * unit);
+        *reinterpret_cast<float2*>(po + (2 * t4 + 1) * kRow + d) = make_float2(acc[mt][1] * unit, acc[mt][3] * unit);
     }
     if (g4 == 0) {
 #pragma unroll

@@ -5,6 +5,8 @@ Attention: with w the weights, an output is sum_t w_t v_t; a relative error d_t 
 normalise) moves it by at most 2 max|d_t| max|v|.  A weight's relative error is ln 2 times the absolute error of
 its base-2 logit plus exp2's (2^-22) plus the rounding of p for the matrix product.  A logit is a sum of D
 products: at most (D + 8) roundings of partial sums no larger than A = max_t sum_i |q_i k_ti| / sqrt(D) * log2 e.
+bf16 queries over the int8 cache are 16-bit fixed point: an element is off by at most Q_PART of the head's largest,
+which moves a logit by at most that times sum_i |k_ti| / sqrt(D) nats (e4m3: fp16, 2^-24 below 2^-14 of 2^14).
 The sum over tokens runs over at most n / 16 + 32 fp32 additions of partial sums no larger than max|v|.
 """
 from __future__ import annotations
@@ -20,6 +22,7 @@ PAGE = 16
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 HALF_STEP = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 P_ROUND = {"bf16": 2.0 ** -11, "f32": 2.0 ** -22}      # p as one fp16 value, or as the sum of two
+Q_PART = {"e4m3": 2.0 ** -39, "int8": 2.0 ** -15}      # half a step of the smallest unit
 PAYLOAD = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
 
 
@@ -32,8 +35,9 @@ def stream():
     return torch.cuda.current_stream().cuda_stream
 
 
-def attention_tolerance(q, K, V, ref, dtype, p_round=None):
-    """Element-wise bound of |kernel - fp64| for q [Hq, D], K and V [Hkv, n, D], ref [Hq, D]."""
+def attention_tolerance(q, K, V, ref, dtype, p_round=None, fmt=None):
+    """Element-wise bound of |kernel - fp64| for q [Hq, D], K and V [Hkv, n, D], ref [Hq, D]; fmt: the 8-bit
+    cache's format."""
     if K.shape[1] == 0:
         return np.zeros_like(ref)
     Hq, D = q.shape
@@ -43,6 +47,8 @@ def attention_tolerance(q, K, V, ref, dtype, p_round=None):
     for h in range(Hq):
         A = float((np.abs(K[h // G]) @ np.abs(q[h])).max()) / math.sqrt(D) * math.log2(math.e)
         rel = math.log(2) * (D + 8) * 2.0 ** -24 * A + 2.0 ** -22 + p_round
+        if fmt is not None and dtype == "bf16":
+            rel += Q_PART[fmt] * np.abs(q[h]).max() * np.abs(K[h // G]).sum(1).max() / math.sqrt(D)
         vmax = np.abs(V[h // G]).max()
         tol[h] = 2 * vmax * rel + (K.shape[1] / 16 + 32) * 2.0 ** -24 * vmax
     # the result itself, and its distance from the exact one, are rounded to the output type

@@ -82,7 +82,7 @@ class Loop:
                 elif kind == "sparse":
                     seen = [x for j in selected[b] for x in range(j * PAGE, min(n, (j + 1) * PAGE))]
                 ref = R.attention(qr[b], K, V, seen)
-                tol = attention_tolerance(qr[b], K[:, seen], V[:, seen], ref, dtype)
+                tol = attention_tolerance(qr[b], K[:, seen], V[:, seen], ref, dtype, fmt=self.cache)
                 assert_within(host(out)[l, b], ref, tol, f"step {t} layer {l} {kind} b={b}")
                 if kind == "delta":
                     s = np.stack([K[h * HKV // HQ] @ qr[b, h] for h in range(HQ)]) / np.sqrt(D)
