@@ -26,7 +26,7 @@
  *   descriptor structs themselves, which are read on the host during the call.
  *   The library allocates nothing and reads no environment variable.  Between
  *   calls it keeps only per-device caches filled on first use and never changed
- *   afterwards (SM count, kernel attributes it set, cluster occupancy, the driver's
+ *   afterwards (SM count, kernel attributes it set, cluster occupancy, split plans, the driver's
  *   tensor-map encoder, the address of delta_full_attn_noalloc's scratch array),
  *   guarded by a mutex; a device reset (cudaDeviceReset) invalidates them, so
  *   reload the library after one.

@@ -41,7 +41,7 @@ SplitPlan plan_q8(int dtype, int batch, int Hkv, int items) {
     const int sms = device_sm_count();
     const bool few_units = units * 16 <= sms && items >= 16 * kQ8WideWarps * 2;
     const bool mid_units = units * 16 > sms && units * 4 <= sms;
-    return plan_q8_variant(batch, Hkv, items, Q8_WIDE && dtype == DELTA_BF16 && ((Q8_WIDE & 1 && few_units) || (Q8_WIDE & 2 && mid_units)) ? kVarWide : kVarNarrow);
+    return plan_q8_variant(batch, Hkv, items, dtype == DELTA_BF16 && (few_units || mid_units) ? kVarWide : kVarNarrow);
 }
 
 WsLayout q8_layout(const delta_desc* d, int batch, int max_pages, bool logits) {

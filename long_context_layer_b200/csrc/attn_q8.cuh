@@ -6,15 +6,10 @@
 
 namespace delta {
 
-// bf16 queries: 8-warp CTAs, two an SM (kVarNarrow), or one 16-warp CTA an SM (kVarWide); the same pages in
-// flight.  fp32 queries carry every fragment twice and keep to 8 warps.
-#ifndef Q8_WIDE
-#define Q8_WIDE 3
-#endif
-#ifndef Q8_STAGES
-#define Q8_STAGES 3
-#endif
-constexpr int kQ8Warps = 8, kQ8WideWarps = 16, kQ8Stages = Q8_STAGES;
+// 6-warp CTAs, two an SM (kVarNarrow), or, bf16 queries, one 12-warp CTA an SM (kVarWide); a warp's ring holds
+// 16 KB of pages (two pairs of pages of head_dim 128).
+constexpr int kQ8Warps = 6, kQ8WideWarps = 12;
+constexpr int q8_stages(int D) { return 512 / D; }
 
 struct Q8Kernel {
     const void* fn;

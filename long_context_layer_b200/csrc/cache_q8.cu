@@ -10,36 +10,49 @@
 
 namespace delta {
 
-constexpr int kBlockWarps = 8;       // warps of a bulk-write / read-back block, one cache block each
-constexpr int kMaxPageBlocks = 16384;   // grid columns; more pages are strided over
+// Bulk calls run one-warp blocks: a block of 8 warps (8 heads of a page) waits for its slowest, 79 instead of
+// 65 us for the write of 4 x 16k tokens of 8 heads (6.2 TB/s; the read back 71 us, 5.7 TB/s).  A warp of a long
+// write takes 4 consecutive pages, whose table entries it looks up at once (one page a warp: 72 us with two
+// warps a block, against 69).
+constexpr int kMaxColumns = 16384;   // grid columns; more pages are strided over
+constexpr int kWarpsPerSm = 64;      // warps an SM gets before a warp takes more than one page
+constexpr int kMaxChunk = 4;
 
-// Writes rows [f0, f1) of a block from src (row f0 first, `stride` elements apart) and rounds its older
-// rows [0, f0) again when the scale grows.  ROWS: most rows written (1: an appended token).
-template <typename T, int D, int FMT, int ROWS>
-__device__ __forceinline__ void write_block(const T* src, int64_t stride, int f0, int f1, uint8_t* block, float* scale,
-                                            int lane) {
-    constexpr int V = Raw16<T>::N;               // elements of a 16-byte load
-    constexpr int LPR = D / V;                   // lanes a row takes
-    constexpr int RPI = 32 / LPR;                // rows of one pass over the lanes
-    constexpr int ITERS = (ROWS + RPI - 1) / RPI;
-    uint4 raw[ITERS];
-    const int r = lane / LPR, c = (lane % LPR) * V;
-    const uint32_t before = f0 > 0 ? __float_as_uint(__ldcg(scale)) & 0x7fffffffu : 0u;
-    uint32_t amax = 0;
+// The lanes of a warp over rows of D elements of T, 16 bytes a lane.
+template <typename T, int D, int ROWS>
+struct Rows {
+    static constexpr int V = Raw16<T>::N;               // elements of a 16-byte load
+    static constexpr int LPR = D / V;                   // lanes a row takes
+    static constexpr int RPI = 32 / LPR;                // rows of one pass over the lanes
+    static constexpr int ITERS = (ROWS + RPI - 1) / RPI;
+};
+
+// Rows [f0, f1) of a block from src (row f0 first, `stride` elements apart); zeros elsewhere.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ void load_rows(const T* src, int64_t stride, int f0, int f1, int lane,
+                                          uint4 (&raw)[Rows<T, D, ROWS>::ITERS]) {
+    using R = Rows<T, D, ROWS>;
+    const int r = lane / R::LPR, c = (lane % R::LPR) * R::V;
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-        const int row = f0 + i * RPI + r;
+    for (int i = 0; i < R::ITERS; ++i) {
+        const int row = f0 + i * R::RPI + r;
         raw[i] = make_uint4(0, 0, 0, 0);
         if (row < f1) raw[i] = *reinterpret_cast<const uint4*>(src + int64_t(row - f0) * stride + c);
     }
+}
+
+// Writes those rows into a block and rounds its older rows [0, f0) again when the scale grows.
+template <typename T, int D, int FMT, int ROWS>
+__device__ __forceinline__ void store_block(const uint4 (&raw)[Rows<T, D, ROWS>::ITERS], int f0, int f1, uint8_t* block,
+                                            float* scale, int lane) {
+    using R = Rows<T, D, ROWS>;
+    constexpr int V = R::V;
+    const int r = lane / R::LPR, c = (lane % R::LPR) * V;
+    const uint32_t before = f0 > 0 ? __float_as_uint(__ldcg(scale)) & 0x7fffffffu : 0u;
+    uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-        float x[V];
-        Raw16<T>::get(raw[i], x);
-#pragma unroll
-        for (int k = 0; k < V; ++k) amax = max(amax, __float_as_uint(x[k]) & 0x7fffffffu);   // NaN > inf > finite
-    }
-    amax = __reduce_max_sync(0xffffffffu, amax);
+    for (int i = 0; i < R::ITERS; ++i) amax = Raw16<T>::more(amax, raw[i]);
+    amax = __reduce_max_sync(0xffffffffu, Raw16<T>::top(amax));
     const uint32_t now = max(before, block_scale_bits<FMT>(amax));
     const bool fine = scale_finite(now);
     const float inv = fine ? scale_inverse(now) : 0.f;
@@ -58,8 +71,8 @@ __device__ __forceinline__ void write_block(const T* src, int64_t stride, int f0
         }
     }
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-        const int row = f0 + i * RPI + r;
+    for (int i = 0; i < R::ITERS; ++i) {
+        const int row = f0 + i * R::RPI + r;
         if (row >= f1) continue;
         float x[V];
         Raw16<T>::get(raw[i], x);
@@ -104,7 +117,9 @@ __global__ void __launch_bounds__(64) append_q8_kernel(const __grid_constant__ A
     if (phys < 0 || phys >= num_phys_pages) return;   // flagged by the attention call that follows
     const T* src = static_cast<const T*>(kv ? a.v_new[l] : a.k_new[l]) + (size_t(b) * Hkv + g) * D;
     const size_t block = size_t(phys) * Hkv + g;
-    write_block<T, D, FMT, 1>(src, 0, slot, slot + 1, (kv ? a.cache[l].pool[1] : a.cache[l].pool[0]) + block * kPage * D,
+    uint4 raw[1];
+    load_rows<T, D, 1>(src, 0, slot, slot + 1, lane, raw);
+    store_block<T, D, FMT, 1>(raw, slot, slot + 1, (kv ? a.cache[l].pool[1] : a.cache[l].pool[0]) + block * kPage * D,
                               (kv ? a.cache[l].scale[1] : a.cache[l].scale[0]) + block, lane);
 }
 
@@ -120,6 +135,7 @@ struct BulkQ8 {
     void* out[2];               // k, v rows (read back)
     Q8Pools cache;
     int32_t Hkv;
+    int32_t chunk;              // consecutive pages a warp takes, 1..32
 };
 
 // The positions [lo, hi) of sequence b that a bulk call covers, and the row of position 0 (may be negative).
@@ -131,87 +147,121 @@ __device__ __forceinline__ void bulk_range(const BulkQ8& p, int b, int64_t& lo, 
     row0 = t0 - first;
 }
 
-// Grid (pages, sequences, groups of 8 (K or V, KV head) items); a warp takes one item of a page.
+// Physical pages of the warp's chunk of logical pages lp0 .. lp0 + cnt - 1, one a lane; -1 where the table or the
+// pool has none (the attention calls flag those).
+__device__ __forceinline__ int chunk_pages(const BulkQ8& p, int b, int lp0, int cnt, int lane) {
+    if (lane >= cnt) return -1;
+    const int pbeg = p.indptr[b], npg = p.indptr[b + 1] - pbeg;
+    if (lp0 + lane >= npg) return -1;
+    const int64_t phys = p.indices[pbeg + lp0 + lane];
+    return phys < 0 || phys >= p.num_phys_pages ? -1 : int(phys);
+}
+
+// Grid (chunks of pages, sequences, (K or V, KV head) items), a warp each.
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kBlockWarps * 32) write_q8_kernel(const BulkQ8 p) {
+__global__ void __launch_bounds__(32) write_q8_kernel(const BulkQ8 p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.y, lane = threadIdx.x & 31;
-    const int item = blockIdx.z * kBlockWarps + (threadIdx.x >> 5);
+    constexpr int ITERS = Rows<T, D, kPage>::ITERS;
+    const int b = blockIdx.y, lane = threadIdx.x, item = blockIdx.z;
     int64_t lo, hi, row0;
     bulk_range(p, b, lo, hi, row0);
-    if (lo < hi && item < 2 * p.Hkv) {
-        const int kv = item & 1, g = item >> 1;
-        const int pbeg = p.indptr[b], npg = p.indptr[b + 1] - pbeg;
-        const int first = int(lo / kPage), last = min(int((hi - 1) / kPage), npg - 1);
-        for (int lp = first + int(blockIdx.x); lp <= last; lp += int(gridDim.x)) {
-            const int64_t phys = p.indices[pbeg + lp];
-            if (phys < 0 || phys >= p.num_phys_pages) continue;   // flagged by the attention calls
-            const int64_t base = int64_t(lp) * kPage;
-            const int f0 = int(max(lo - base, int64_t(0))), f1 = int(min(hi - base, int64_t(kPage)));
-            const T* src = static_cast<const T*>(kv ? p.in[1] : p.in[0]) + (row0 + base + f0) * p.stride + int64_t(g) * D;
-            const size_t block = size_t(phys) * p.Hkv + g;
-            write_block<T, D, FMT, kPage>(src, p.stride, f0, f1, (kv ? p.cache.pool[1] : p.cache.pool[0]) + block * kPage * D,
-                                          (kv ? p.cache.scale[1] : p.cache.scale[0]) + block, lane);
+    if (lo < hi) {
+        const int kv = item >= p.Hkv ? 1 : 0, g = item - kv * p.Hkv;
+        const T* in = static_cast<const T*>(kv ? p.in[1] : p.in[0]) + int64_t(g) * D;
+        uint8_t* pool = (kv ? p.cache.pool[1] : p.cache.pool[0]);
+        float* scale = (kv ? p.cache.scale[1] : p.cache.scale[0]);
+        const int first = int(lo / kPage), last = int((hi - 1) / kPage);
+        for (int64_t at = first + int64_t(blockIdx.x) * p.chunk; at <= last; at += int64_t(gridDim.x) * p.chunk) {
+            const int lp0 = int(at), cnt = min(p.chunk, last - lp0 + 1);
+            auto range = [&](int lp, int& f0, int& f1) {
+                f0 = int(max(lo - int64_t(lp) * kPage, int64_t(0)));
+                f1 = int(min(hi - int64_t(lp) * kPage, int64_t(kPage)));
+            };
+            auto load = [&](int lp, uint4 (&raw)[ITERS]) {
+                int f0, f1;
+                range(lp, f0, f1);
+                load_rows<T, D, kPage>(in + (row0 + int64_t(lp) * kPage + f0) * p.stride, p.stride, f0, f1, lane, raw);
+            };
+            uint4 raw[ITERS];
+            load(lp0, raw);
+            const int pages = chunk_pages(p, b, lp0, cnt, lane);
+            for (int i = 0; i < cnt; ++i) {
+                const int phys = __shfl_sync(0xffffffffu, pages, i);
+                if (phys >= 0) {
+                    int f0, f1;
+                    range(lp0 + i, f0, f1);
+                    const size_t block = size_t(phys) * p.Hkv + g;
+                    store_block<T, D, FMT, kPage>(raw, f0, f1, pool + block * kPage * D, scale + block, lane);
+                }
+                if (i + 1 < cnt) load(lp0 + i + 1, raw);
+            }
         }
     }
     // The next kernel may load pages (through the asynchronous proxy) before it waits for this grid;
-    // it is not started before every block is done, and these fences put the writes ahead of that.
-    __threadfence();
-    asm volatile("fence.proxy.async.global;" ::: "memory");
+    // it is not started before every block is done, and these fences put the warp's writes ahead of
+    // that (one lane's, behind the warp barrier).
+    __syncwarp();
+    if (lane == 0) {
+        __threadfence();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+    }
 }
 
+// The same grid, a page at a time: the payload is 16 bytes a lane and pass.
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kBlockWarps * 32) read_q8_kernel(const BulkQ8 p) {
+__global__ void __launch_bounds__(32) read_q8_kernel(const BulkQ8 p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.y, lane = threadIdx.x & 31;
-    const int item = blockIdx.z * kBlockWarps + (threadIdx.x >> 5);
+    const int b = blockIdx.y, lane = threadIdx.x, item = blockIdx.z;
     int64_t lo, hi, row0;
     bulk_range(p, b, lo, hi, row0);
-    if (lo >= hi || item >= 2 * p.Hkv) return;
-    constexpr int LPR = D / 16, RPI = 32 / LPR, ITERS = kPage / RPI;   // 16 payload bytes a lane
-    const int kv = item & 1, g = item >> 1;
+    if (lo >= hi) return;
+    constexpr int LPR = D / 16, RPI = 32 / LPR, ITERS = kPage / RPI;
+    const int kv = item >= p.Hkv ? 1 : 0, g = item - kv * p.Hkv;
     const int r = lane / LPR, c = (lane % LPR) * 16;
+    const uint8_t* pool = (kv ? p.cache.pool[1] : p.cache.pool[0]);
+    const float* scale = (kv ? p.cache.scale[1] : p.cache.scale[0]);
+    T* out = static_cast<T*>(kv ? p.out[1] : p.out[0]) + int64_t(g) * D + c;
     const int pbeg = p.indptr[b], npg = p.indptr[b + 1] - pbeg;
     const int first = int(lo / kPage), last = min(int((hi - 1) / kPage), npg - 1);
-    for (int lp = first + int(blockIdx.x); lp <= last; lp += int(gridDim.x)) {
+    for (int64_t lp = first + int64_t(blockIdx.x); lp <= last; lp += gridDim.x) {
         const int64_t phys = p.indices[pbeg + lp];
-        if (phys < 0 || phys >= p.num_phys_pages) continue;
+        if (phys < 0 || phys >= p.num_phys_pages) continue;     // flagged by the attention calls
         const size_t block = size_t(phys) * p.Hkv + g;
-        const uint8_t* src = (kv ? p.cache.pool[1] : p.cache.pool[0]) + block * kPage * D;
         uint4 w[ITERS];
 #pragma unroll
-        for (int i = 0; i < ITERS; ++i) w[i] = *reinterpret_cast<const uint4*>(src + (i * RPI + r) * D + c);
-        const float s = (kv ? p.cache.scale[1] : p.cache.scale[0])[block];
+        for (int i = 0; i < ITERS; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(pool + block * kPage * D + (i * RPI + r) * D + c);
+        const float s = scale[block];
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
-            const int64_t pos = int64_t(lp) * kPage + i * RPI + r;
+            const int64_t pos = lp * kPage + i * RPI + r;
             if (pos < lo || pos >= hi) continue;
-            T* dst = static_cast<T*>(kv ? p.out[1] : p.out[0]) + (row0 + pos) * p.stride + int64_t(g) * D + c;
+            T* dst = out + (row0 + pos) * p.stride;
             const uint32_t* u = reinterpret_cast<const uint32_t*>(&w[i]);
             float x[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 a = unpack8x2<FMT>(u[k]), d = unpack8x2<FMT>(u[k] >> 16);
-                x[4 * k] = a.x * s;
-                x[4 * k + 1] = a.y * s;
-                x[4 * k + 2] = d.x * s;
-                x[4 * k + 3] = d.y * s;
+            for (int j = 0; j < 4; ++j) {
+                const float2 a = unpack8x2<FMT>(u[j]), d = unpack8x2<FMT>(u[j] >> 16);
+                x[4 * j] = a.x * s;
+                x[4 * j + 1] = a.y * s;
+                x[4 * j + 2] = d.x * s;
+                x[4 * j + 3] = d.y * s;
             }
             if constexpr (sizeof(T) == 2) {
                 uint4 o[2];
                 uint32_t* q = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-                    q[k] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int j = 0; j < 8; ++j) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                    q[j] = *reinterpret_cast<const uint32_t*>(&h);
                 }
                 reinterpret_cast<uint4*>(dst)[0] = o[0];
                 reinterpret_cast<uint4*>(dst)[1] = o[1];
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    reinterpret_cast<float4*>(dst)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<float4*>(dst)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
             }
         }
     }
@@ -251,8 +301,8 @@ struct LaunchBulk {
     cudaStream_t st;
     template <typename T, int D, int FMT>
     delta_status operator()() const {
-        return write ? launch_pdl(write_q8_kernel<T, D, FMT>, grid, dim3(kBlockWarps * 32), 0, st, p)
-                     : launch_pdl(read_q8_kernel<T, D, FMT>, grid, dim3(kBlockWarps * 32), 0, st, p);
+        return write ? launch_pdl(write_q8_kernel<T, D, FMT>, grid, dim3(32), 0, st, p)
+                     : launch_pdl(read_q8_kernel<T, D, FMT>, grid, dim3(32), 0, st, p);
     }
 };
 
@@ -316,8 +366,11 @@ delta_status bulk(const delta_desc* desc, const delta_page_table* pt, const int3
     p.Hkv = desc->num_kv_heads;
     // max_tokens tokens overlap at most one page more than they fill
     const int64_t pages = (int64_t(max_tokens) + kPage - 1) / kPage + 1;
-    const dim3 grid(unsigned(pages < kMaxPageBlocks ? pages : kMaxPageBlocks), pt->batch,
-                    (2 * desc->num_kv_heads + kBlockWarps - 1) / kBlockWarps);
+    const int items = 2 * desc->num_kv_heads;
+    const int64_t warps = pages * pt->batch * items / (int64_t(device_sm_count()) * kWarpsPerSm);
+    p.chunk = !write || warps < 1 ? 1 : warps > kMaxChunk ? kMaxChunk : int(warps);
+    const int64_t columns = (pages + p.chunk - 1) / p.chunk;
+    const dim3 grid(unsigned(columns < kMaxColumns ? columns : kMaxColumns), pt->batch, items);
     return for_types(desc, cache->format, LaunchBulk{p, grid, write, static_cast<cudaStream_t>(stream)});
 }
 

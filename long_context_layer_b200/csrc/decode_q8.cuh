@@ -40,6 +40,7 @@ struct Q8Smem {
     static constexpr size_t kStages = size_t(WARPS) * STAGES * kPage2;
     static_assert(size_t(STAGES) * kPage2 >= (size_t(kMaxGroup) * (D + 4) + 4 * kMaxGroup) * sizeof(float), "merge record");
     static constexpr size_t kBars = size_t(WARPS) * STAGES * sizeof(uint64_t);
+    static_assert(kBars % 16 == 0, "the merge's receive area starts on 16 bytes");
     static constexpr size_t kRecv = size_t(recv_floats<D>()) * sizeof(float);
     static constexpr size_t kBytes = 1024 /* alignment slack */ + kStages + kBars + kRecv;
 };
@@ -120,7 +121,8 @@ struct Q8Pages {
     float ks_a, vs_a, ks_b, vs_b;
 };
 
-template <int W>
+// QUIET: a speculative lookup before the wait, which raises no flags.
+template <int W, bool QUIET = false>
 __device__ __forceinline__ void q8_lookup(const DecodeParams& p, const SeqExtent& ex, int b, int i0, int warp, int nk,
                                           int kbase, int lane, int& lp, int& ph) {
     const int k = kbase + lane;
@@ -130,13 +132,13 @@ __device__ __forceinline__ void q8_lookup(const DecodeParams& p, const SeqExtent
     const int i = i0 + warp + k * W;
     lp = p.mode == kModeSparse ? __ldcg(p.sel_pages + size_t(b) * p.sel_stride + i) : p.mode == kModeWindow ? window_page(ex, i) : i;
     if (lp < 0 || lp >= ex.N) {
-        atomicOr(p.err, kErrSel);
+        if (!QUIET) atomicOr(p.err, kErrSel);
         lp = -1;
         return;
     }
     const int64_t x = p.indices[ex.pbeg + lp];
     if (x < 0 || x >= p.num_phys_pages) {
-        atomicOr(p.err, kErrPage);
+        if (!QUIET) atomicOr(p.err, kErrPage);
         lp = -1;
         return;
     }
@@ -240,26 +242,61 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
 
     if (threadIdx.x == 0)
         prefetch_l2(reinterpret_cast<const T*>(p.q) + (size_t(b) * Hq + h0) * D, G * D * sizeof(T));
-    // Before the wait: every page but the newest (all of a settled selection); the first sparse layer behind
-    // a delta-layer waits, its page list is that layer's output.
+    // Before the wait: every page but the newest (all of a settled selection).  The first sparse layer behind a
+    // delta-layer guesses that the selection is already the new one (mostly the last step's still holds) and
+    // checks it after the wait.
     const bool known = p.mode != kModeSparse || p.settled;
     uint32_t early = 0;       // bit k: page k's copies were issued before the wait
+    uint32_t parity = 0;      // of the phases of the pages in hand
     if (known) {
         setup(newest);
-        for (int k = 0; k < min(STAGES, nk); ++k) {
-            const int lp = __shfl_sync(0xffffffffu, pages.lp_a, k);
-            if (lp >= 0 && lp != newest) {
-                issue(k, k);
-                early |= 1u << k;
-            }
+    } else {
+        ex.count = min(max(__ldcg(p.sel_cnt + b), 0), min(p.sel_stride, p.items_per_split * p.num_splits));
+        i0 = split * p.items_per_split;
+        const int i1 = min(i0 + p.items_per_split, ex.count);
+        nk = (i1 - i0 > warp) ? (i1 - i0 - warp + WARPS - 1) / WARPS : 0;
+        pages.cur = 0;
+        q8_lookup<WARPS, true>(p, ex, b, i0, warp, nk, 0, lane, pages.lp_a, pages.ph_a);
+        q8_scales(p, g, pages.lp_a, pages.ph_a, newest, pages.ks_a, pages.vs_a);
+        pages.lp_b = pages.ph_b = -1;
+    }
+    for (int k = 0; k < min(STAGES, nk); ++k) {
+        const int lp = __shfl_sync(0xffffffffu, pages.lp_a, k);
+        if (lp >= 0 && lp != newest) {
+            issue(k, k);
+            early |= 1u << k;
         }
     }
     pdl_wait();
     pdl_trigger();
-    if (!known) setup(-1);
+    if (!known) {
+        // the selection's entries at the guessed places, loaded together with its count
+        const int guess_nk = nk;
+        const int lp = lane < nk ? __ldcg(p.sel_pages + size_t(b) * p.sel_stride + i0 + warp + lane * WARPS) : -1;
+        seq_count(p, b, ex);
+        const int i1 = min(i0 + p.items_per_split, ex.count);
+        nk = (i1 - i0 > warp) ? (i1 - i0 - warp + WARPS - 1) / WARPS : 0;
+        if (nk == guess_nk && __all_sync(0xffffffffu, lane >= nk || (lp == pages.lp_a && lp >= 0))) {
+            q8_lookup<WARPS>(p, ex, b, i0, warp, nk, 32, lane, pages.lp_b, pages.ph_b);
+            q8_scales(p, g, pages.lp_b, pages.ph_b, -1, pages.ks_b, pages.vs_b);
+        } else {
+            // spend the first phase of every stage: wait for the guessed copies (bounded), pass the others
+            for (int k = 0; k < STAGES; ++k) {
+                if ((early >> k) & 1u) {
+                    if (!mbar_wait(&wbar[k], 0) && lane == 0) atomicOr(p.err, kErrTimeout);
+                } else {
+                    if (lane == 0) mbar_arrive(&wbar[k]);
+                }
+            }
+            __syncwarp();
+            early = 0;
+            parity = 1;
+            setup(-1);
+        }
+    }
     for (int k = 0; k < min(STAGES, nk); ++k)
         if (!((early >> k) & 1u)) issue(k, k);
-    if (known && newest >= 0) {   // the newest page's scales, if this lane holds it
+    if (newest >= 0) {   // the newest page's scales, if this lane holds it
         if (pages.lp_a == newest) q8_scales(p, g, pages.lp_a, pages.ph_a, -1, pages.ks_a, pages.vs_a);
         if (pages.lp_b == newest) q8_scales(p, g, pages.lp_b, pages.ph_b, -1, pages.ks_b, pages.vs_b);
     }
@@ -463,9 +500,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         }
     };
 
-    // stages of the pages in hand and the parity of their phases (page k: stage k % STAGES, phase k / STAGES)
-    int sA = 0;
-    uint32_t parity = 0;
+    const uint32_t parity0 = parity;
+    int sA = 0;               // stage of page k: k % STAGES
     for (int k = 0; k < nk; k += 2) {
         advance(k);
         const bool two = k + 1 < nk;
@@ -565,7 +601,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     }
     if (failed) {
         // drain this warp's copies still in flight (bounded) before shared memory is released
-        for (int k = consumed + 1; k < min(consumed + STAGES, nk); ++k) mbar_wait(&wbar[k % STAGES], (k / STAGES) & 1);
+        for (int k = consumed + 1; k < min(consumed + STAGES, nk); ++k)
+            mbar_wait(&wbar[k % STAGES], parity0 ^ ((k / STAGES) & 1));
     }
     const float unit = vref * kUnshift;      // of the accumulators
 #pragma unroll

@@ -198,7 +198,7 @@ inline int max_active_clusters(const void* func, size_t smem, int cluster, int t
 // cluster merge (a unit spread over several clusters needs a second arrival stage).
 // kernel_of(variant, &smem, &threads): the kernel of that variant, its dynamic shared memory and threads.
 template <typename KernelOf>
-inline SplitPlan fit_plan(SplitPlan pl, const KernelOf& kernel_of, int units, int items, bool one_cluster_per_unit = false) {
+SplitPlan fit_plan_now(SplitPlan pl, const KernelOf& kernel_of, int units, int items, bool one_cluster_per_unit = false) {
     const int s = pl.splits();
     // Clusters meet through the workspace only when each gets at least 256 pages (and the unit has
     // more than 512): below that the cross-cluster merge costs more than the extra CTAs gain.
@@ -234,6 +234,38 @@ inline SplitPlan fit_plan(SplitPlan pl, const KernelOf& kernel_of, int units, in
         best.variant = kVarNarrow;
     }
     return best;
+}
+
+// fit_plan_now, remembered: a plan depends on the kernel and the sizes alone, and finding it asks for the cluster
+// occupancy up to 16 times.
+struct KnownPlan {
+    const void* fn;
+    int dev, cluster, clusters, units, items, one;
+    SplitPlan plan;
+};
+template <typename KernelOf>
+SplitPlan fit_plan(SplitPlan pl, const KernelOf& kernel_of, int units, int items, bool one_cluster_per_unit = false) {
+    constexpr int kSlots = 256;
+    static KnownPlan known[kSlots];
+    static int count = 0;
+    size_t smem = 0;
+    int threads = 0;
+    const int dev = current_device();
+    const KnownPlan key = {kernel_of(pl.variant, &smem, &threads), dev, pl.cluster, pl.clusters, units, items,
+                           one_cluster_per_unit ? 1 : 0, pl};
+    std::lock_guard<std::recursive_mutex> lock(cache_mutex());
+    for (int i = count - 1; i >= 0; --i) {
+        const KnownPlan& k = known[i];
+        if (k.fn == key.fn && k.dev == key.dev && k.units == key.units && k.items == key.items && k.one == key.one &&
+            k.cluster == key.cluster && k.clusters == key.clusters)
+            return k.plan;
+    }
+    const SplitPlan plan = fit_plan_now(pl, kernel_of, units, items, one_cluster_per_unit);
+    if (dev >= 0 && count < kSlots) {
+        known[count] = key;
+        known[count++].plan = plan;
+    }
+    return plan;
 }
 
 // Launch with programmatic dependent launch: the kernel may be scheduled while the previous

@@ -68,10 +68,21 @@ struct Raw16<__nv_bfloat16> {
         unpack_bf16x2(w.z, x[4], x[5]);
         unpack_bf16x2(w.w, x[6], x[7]);
     }
+    // Running largest magnitude as bits (NaN > infinity > finite), two halfwords at once; top() is one float's.
+    static __device__ __forceinline__ uint32_t more(uint32_t m, uint4 w) {
+        m = __vimax3_u16x2(m, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+        return __vimax3_u16x2(m, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
+    }
+    static __device__ __forceinline__ uint32_t top(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
 };
 template <>
 struct Raw16<float> {
     static constexpr int N = 4;
+    static __device__ __forceinline__ uint32_t more(uint32_t m, uint4 w) {
+        m = __vimax3_u32(m, w.x & 0x7fffffffu, w.y & 0x7fffffffu);
+        return __vimax3_u32(m, w.z & 0x7fffffffu, w.w & 0x7fffffffu);
+    }
+    static __device__ __forceinline__ uint32_t top(uint32_t m) { return m; }
     static __device__ __forceinline__ void get(uint4 w, float (&x)[4]) {
         x[0] = __uint_as_float(w.x);
         x[1] = __uint_as_float(w.y);
