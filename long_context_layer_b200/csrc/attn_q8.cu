@@ -20,10 +20,10 @@ bool make_block_map(CUtensorMap* map, const void* pool, const delta_desc* d) {
 }
 
 // About one wave of CTAs, at least a page per warp.
-SplitPlan plan_q8_variant(int batch, int Hkv, int items, int variant) {
+SplitPlan plan_q8_variant(int D, int batch, int Hkv, int items, int variant) {
     if (items <= 0) return {1, 1, kVarNarrow};
     const bool wide = variant == kVarWide;
-    const int warps = wide ? kQ8WideWarps : kQ8Warps;
+    const int warps = q8_warps(D, wide);
     const int slots = device_sm_count() * (wide ? 1 : 2);
     int s = slots / (batch * Hkv);
     const int per_cta = wide ? warps : 2 * warps - 1;
@@ -36,17 +36,20 @@ SplitPlan plan_q8_variant(int batch, int Hkv, int items, int variant) {
     return pl;
 }
 
-SplitPlan plan_q8(int dtype, int batch, int Hkv, int items) {
+// One wide CTA an SM where plan_splits has one for the bf16 cache, by the same rules: a full cluster for each of a
+// few units with long lists (one sequence: 8k full layer 7.7 instead of 8.3 us, 32k 20 instead of 24.5), and
+// mid-size batches (4 x 64k 84 instead of 91 us, 2 x 4k 8.6 instead of 10.6); else two narrow ones.
+SplitPlan plan_q8(int dtype, int D, int batch, int Hkv, int items) {
     const int64_t units = int64_t(batch) * Hkv;
     const int sms = device_sm_count();
-    const bool few_units = units * 16 <= sms && items >= 16 * kQ8WideWarps * 2;
+    const bool few_units = units * 16 <= sms && items >= 16 * q8_warps(D, true) * 2;
     const bool mid_units = units * 16 > sms && units * 4 <= sms;
-    return plan_q8_variant(batch, Hkv, items, dtype == DELTA_BF16 && (few_units || mid_units) ? kVarWide : kVarNarrow);
+    return plan_q8_variant(D, batch, Hkv, items, dtype == DELTA_BF16 && (few_units || mid_units) ? kVarWide : kVarNarrow);
 }
 
 WsLayout q8_layout(const delta_desc* d, int batch, int max_pages, bool logits) {
-    const int a = plan_q8_variant(batch, d->num_kv_heads, max_pages, kVarNarrow).splits();
-    const int b = plan_q8_variant(batch, d->num_kv_heads, max_pages, kVarWide).splits();
+    const int a = plan_q8_variant(d->head_dim, batch, d->num_kv_heads, max_pages, kVarNarrow).splits();
+    const int b = plan_q8_variant(d->head_dim, batch, d->num_kv_heads, max_pages, kVarWide).splits();
     return ws_layout_splits(d, batch, max_pages, a > b ? a : b, logits);
 }
 
@@ -66,7 +69,7 @@ struct Q8Cache {
             *threads = k.threads;
             return k.fn;
         };
-        return fit_plan(plan_q8(dtype, batch, Hkv, items), kernel_of, batch * Hkv, items, fused);
+        return fit_plan(plan_q8(dtype, D, batch, Hkv, items), kernel_of, batch * Hkv, items, fused);
     }
     void fill(DecodeParams& prm) const {
         prm.k_pool = c->k_pool;

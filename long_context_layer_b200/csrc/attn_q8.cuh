@@ -6,10 +6,13 @@
 
 namespace delta {
 
-// 6-warp CTAs, two an SM (kVarNarrow), or, bf16 queries, one 12-warp CTA an SM (kVarWide); a warp's ring holds
-// 16 KB of pages (two pairs of pages of head_dim 128).
-constexpr int kQ8Warps = 6, kQ8WideWarps = 12;
-constexpr int q8_stages(int D) { return 512 / D; }
+// Narrow CTAs, two an SM (kVarNarrow), or, bf16 queries, one CTA of twice the warps an SM (kVarWide).  A warp's ring
+// holds 4 pages: while a pair of pages is worked on, the next pair is on its way.  head_dim 128: 6 warps, 96 KB a
+// CTA (8 warps with 3 pages: 16 x 16k sparse layer 20 instead of 18.6 us, full layers alike).  head_dim 64: the
+// pages are half as large for nearly the same work, so 8 warps (16 x 16k full layer 51 us; 6 warps with 8 pages
+// 60, 10 warps 52).
+constexpr int q8_warps(int D, bool wide) { return (D == 128 ? 6 : 8) * (wide ? 2 : 1); }
+constexpr int kQ8Stages = 4;
 
 struct Q8Kernel {
     const void* fn;

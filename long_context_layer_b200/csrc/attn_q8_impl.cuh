@@ -8,13 +8,14 @@ namespace {
 
 template <typename T, int D, int G, int WARPS>
 Q8Kernel entry() {
-    return {reinterpret_cast<const void*>(decode_q8_kernel<T, DELTA_Q8_FMT, D, G, q8_stages(D), WARPS>),
-            Q8Smem<D, q8_stages(D), WARPS>::kBytes, WARPS * 32};
+    return {reinterpret_cast<const void*>(decode_q8_kernel<T, DELTA_Q8_FMT, D, G, kQ8Stages, WARPS>),
+            Q8Smem<D, kQ8Stages, WARPS>::kBytes, WARPS * 32};
 }
 template <int D, int G>
 Q8Kernel by_variant(int dtype, int variant) {
-    if (dtype == DELTA_F32) return entry<float, D, G, kQ8Warps>();
-    return variant == kVarWide ? entry<__nv_bfloat16, D, G, kQ8WideWarps>() : entry<__nv_bfloat16, D, G, kQ8Warps>();
+    if (dtype == DELTA_F32) return entry<float, D, G, q8_warps(D, false)>();
+    return variant == kVarWide ? entry<__nv_bfloat16, D, G, q8_warps(D, true)>()
+                               : entry<__nv_bfloat16, D, G, q8_warps(D, false)>();
 }
 template <int D>
 Q8Kernel by_group(int dtype, int G, int variant) {

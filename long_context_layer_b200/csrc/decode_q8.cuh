@@ -16,13 +16,14 @@
 //        fp32 queries: the fp16 form with a query as the sum of two values (22 bits and the sign).
 //   s = S * (Q's factor per head) * (K's block scale): powers of two and the softmax scale, in fp32.
 //   online softmax as in decode_mma.cuh, with p = 2^(s - m + 14) so that fp16 holds small probabilities
-//        (to 2^-39 of the largest; the offset cancels in o = acc / l), l summed from the rounded p that
-//        weigh V (fp32: p too is a sum of two fp16 values).
-//   O^T[D x 8] += (V's block scale) * V8^T[D x 16] . P^T[16 x 8]   ldmatrix.trans moves 2-byte units, that is
+//        (to 2^-38 of the largest; the offset cancels in o = acc / l).  l sums the fp32 terms, which are also the
+//        page terms of a delta-layer (fp32 outputs: p as the sum of two fp16 values).
+//   O^T[D x 8] += V8^T[D x 16] . (V's block scale / unit * P^T)[16 x 8]   ldmatrix.trans moves 2-byte units, that is
 //        two dimensions of one token; a byte permute separates them, and the accumulator's rows g4 and g4 + 8
 //        are dimensions 2 g4 and 2 g4 + 1 of the 16-dimension tile.
-// Block scales stay out of the fp16 operands (their range is 2^-100..2^122): K's multiplies the logits and V's
-// the page's product before it joins the fp32 accumulator.
+// Block scales range over 2^-100..2^122: K's multiplies the logits; V's joins P relative to the accumulators' unit,
+// the largest scale so far.  (Scaling the product instead costs 64 multiply-adds a pair of pages: about a third
+// of the pages of caches with ordinary spread differ from the unit, 310 instead of 267 instructions a page.)
 #pragma once
 
 #include "decode_mma.cuh"
@@ -306,16 +307,30 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     uint32_t qa[KS], qc[KS], qx[kTwo ? KS : 1], qy[kTwo ? KS : 1];
     float qf0, qf1;           // factors of this lane's logits (heads 2 t4, 2 t4 + 1)
     {
-        float q[KS][4];
+        // bf16: two registers of two; fp32: four
+        uint32_t raw[KS][kTwo ? 4 : 2];
         const T* qp = reinterpret_cast<const T*>(p.q) + (size_t(b) * Hq + h0 + g4) * D + 4 * t4;
         uint32_t amax = 0;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
-            if (g4 < G) load_row<T, 4>(qp + kk * 16, q[kk]);
-            else q[kk][0] = q[kk][1] = q[kk][2] = q[kk][3] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(q[kk][j]) & 0x7fffffffu);
+            if constexpr (kTwo) {
+                const uint4 w = g4 < G ? *reinterpret_cast<const uint4*>(qp + kk * 16) : make_uint4(0, 0, 0, 0);
+                raw[kk][0] = w.x;
+                raw[kk][1] = w.y;
+                raw[kk][2] = w.z;
+                raw[kk][3] = w.w;
+            } else {
+                const uint2 w = g4 < G ? *reinterpret_cast<const uint2*>(qp + kk * 16) : make_uint2(0, 0);
+                raw[kk][0] = w.x;
+                raw[kk][1] = w.y;
+            }
         }
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+            if constexpr (kTwo) amax = Raw16<float>::more(amax, make_uint4(raw[kk][0], raw[kk][1], raw[kk][2], raw[kk][3]));
+            else amax = __vimax3_u16x2(amax, raw[kk][0] & 0x7fff7fffu, raw[kk][1] & 0x7fff7fffu);
+        }
+        if constexpr (!kTwo) amax = Raw16<__nv_bfloat16>::top(amax);
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // 2^x <= |q|max < 2^(x + 1), x at least -100; a head with a non-finite query gives NaN logits
@@ -325,24 +340,31 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         const float factor = fine ? p.qscale * __uint_as_float(uint32_t(x - kTop + 127) << 23) : __uint_as_float(0x7fc00000u);
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
+            float q[4];
+            if constexpr (kTwo) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[kk][j] = fine ? q[kk][j] * up : 0.f;
+                for (int j = 0; j < 4; ++j) q[j] = __uint_as_float(raw[kk][j]);
+            } else {
+                unpack_bf16x2(raw[kk][0], q[0], q[1]);
+                unpack_bf16x2(raw[kk][1], q[2], q[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = fine ? q[j] * up : 0.f;
             if constexpr (kHalf) {
-                qa[kk] = pack_f16(q[kk][0], q[kk][1]);
-                qc[kk] = pack_f16(q[kk][2], q[kk][3]);
+                qa[kk] = pack_f16(q[0], q[1]);
+                qc[kk] = pack_f16(q[2], q[3]);
                 if constexpr (kTwo) {
                     const float2 ra = unpack_f16(qa[kk]), rc = unpack_f16(qc[kk]);
-                    qx[kk] = pack_f16(q[kk][0] - ra.x, q[kk][1] - ra.y);
-                    qy[kk] = pack_f16(q[kk][2] - rc.x, q[kk][3] - rc.y);
+                    qx[kk] = pack_f16(q[0] - ra.x, q[1] - ra.y);
+                    qy[kk] = pack_f16(q[2] - rc.x, q[3] - rc.y);
                 }
             } else {
-                qa[kk] = qc[kk] = 0;
+                // the nearest integer (within +-2^15 - 128) in the low 16 bits of q + 1.5 * 2^23
+                uint32_t i[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = __float2int_rn(q[kk][j]);       // within +-2^15 - 128
-                    qa[kk] |= (uint32_t(i >> 8) & 0xffu) << (8 * j);
-                    qc[kk] |= (uint32_t(i) & 0xffu) << (8 * j);
-                }
+                for (int j = 0; j < 4; ++j) i[j] = __float_as_uint(q[j] + 12582912.f);
+                qa[kk] = __byte_perm(__byte_perm(i[0], i[1], 0x0051), __byte_perm(i[2], i[3], 0x0051), 0x5410);
+                qc[kk] = __byte_perm(__byte_perm(i[0], i[1], 0x0040), __byte_perm(i[2], i[3], 0x0040), 0x5410);
             }
         }
         qf0 = __shfl_sync(0xffffffffu, factor, 8 * t4);
@@ -352,11 +374,11 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     // reference of the base-2 logits of heads 2 t4, 2 t4 + 1 (within 1 below their maximum or above it)
     float m_run[2] = {-3.402823466e38f, -3.402823466e38f};
     float l_run[2] = {0.f, 0.f};               // this lane's tokens only; summed over the lanes at the end
-    float dl_run[2] = {0.f, 0.f};              // delta-layers: the same over the unrounded terms
     float acc[KS][4];
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-    float vref = 1.175494351e-38f;             // unit of acc: the largest V scale so far
+    float vref = 1.175494351e-38f;             // unit of acc: the largest V scale so far (from 2^-126)
+    float vinv = 8.507059173e37f;              // 1 / vref
 
     // ldmatrix roles of this lane: matrix lj = (rows 8 (lj & 1) .. + 7, 16-byte chunk 2 c + (lj >> 1))
     const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
@@ -427,11 +449,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     const bool pick_b = lane & 16, pick_1 = lane & 8;
     const int lse_head = 2 * t4 + (pick_1 ? 1 : 0);
     float* lse_row = p.page_lse + (size_t(b) * Hq + h0 + (lse_head < G ? lse_head : 0)) * p.max_pages;
-    auto page_partials = [&](const float (&pa)[4], const float (&pb)[4], float mn0, float mn1, float al0, float al1,
-                             int lpA, int lpB) {
+    auto page_partials = [&](const float (&pa)[4], const float (&pb)[4], float mn0, float mn1, int lpA, int lpB) {
         const float ea0 = pa[0] + pa[2], ea1 = pa[1] + pa[3], eb0 = pb[0] + pb[2], eb1 = pb[1] + pb[3];
-        dl_run[0] = dl_run[0] * al0 + (ea0 + eb0);
-        dl_run[1] = dl_run[1] * al1 + (ea1 + eb1);
         float e0 = pick_b ? eb0 : ea0, e1 = pick_b ? eb1 : ea1;
         e0 += __shfl_xor_sync(0xffffffffu, pick_b ? ea0 : eb0, 16);
         e1 += __shfl_xor_sync(0xffffffffu, pick_b ? ea1 : eb1, 16);
@@ -460,9 +479,22 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         mma_f16_16816(d1, a0, a1, a2, a3, pt[0], pt[1]);
         if constexpr (kTwo) mma_f16_16816(d1, a0, a1, a2, a3, pt[2], pt[3]);
     };
-    // A page whose V scale is not the accumulators' unit (the largest scale so far).  Powers of two: exact.
-    auto pv_rescaled = [&](int s, const uint32_t (&pt)[kTwo ? 4 : 2], float vs) {
-        if (!(fabsf(vs) <= vref)) {      // a larger unit (or NaN)
+    // the probabilities of a page, times w, as P^T fragments
+    auto round_p = [&](const float (&e)[4], float w, uint32_t (&pt)[kTwo ? 4 : 2]) {
+        const float x[4] = {e[0] * w, e[1] * w, e[2] * w, e[3] * w};
+        const uint32_t x0 = pack_f16(x[0], x[1]), x1 = pack_f16(x[2], x[3]);
+        pt[0] = movmatrix_trans(x0);
+        pt[1] = movmatrix_trans(x1);
+        if constexpr (kTwo) {
+            const float2 r0 = unpack_f16(x0), r1 = unpack_f16(x1);
+            pt[2] = movmatrix_trans(pack_f16(x[0] - r0.x, x[1] - r0.y));
+            pt[3] = movmatrix_trans(pack_f16(x[2] - r1.x, x[3] - r1.y));
+        }
+    };
+    // A page whose V scale does not go with the accumulators' unit (the largest scale so far): a larger one, which
+    // becomes the unit, or one below 2^-20 of it (or NaN), whose product is scaled in fp32.
+    auto pv_rescaled = [&](int s, const float (&e)[4], float vs) {
+        if (!(fabsf(vs) <= vref)) {
             const float r = vref / fabsf(vs);
             vref = fabsf(vs);
 #pragma unroll
@@ -471,6 +503,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
                 for (int j = 0; j < 4; ++j) acc[mt][j] *= r;
         }
         const float w = vs / vref;
+        uint32_t pt[kTwo ? 4 : 2];
+        round_p(e, 1.f, pt);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -481,23 +515,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
                 acc[2 * c + 1][j] = fmaf(d1[j], w, acc[2 * c + 1][j]);
             }
         }
-    };
-    // the rounded probabilities of a page as P^T fragments; adds them to this lane's sums
-    auto round_p = [&](const float (&e)[4], uint32_t (&pt)[kTwo ? 4 : 2], float& s0, float& s1) {
-        const uint32_t x0 = pack_f16(e[0], e[1]), x1 = pack_f16(e[2], e[3]);
-        const float2 r0 = unpack_f16(x0), r1 = unpack_f16(x1);
-        s0 += r0.x + r1.x;
-        s1 += r0.y + r1.y;
-        pt[0] = movmatrix_trans(x0);
-        pt[1] = movmatrix_trans(x1);
-        if constexpr (kTwo) {
-            const uint32_t y0 = pack_f16(e[0] - r0.x, e[1] - r0.y), y1 = pack_f16(e[2] - r1.x, e[3] - r1.y);
-            const float2 u0 = unpack_f16(y0), u1 = unpack_f16(y1);
-            s0 += u0.x + u1.x;
-            s1 += u0.y + u1.y;
-            pt[2] = movmatrix_trans(y0);
-            pt[3] = movmatrix_trans(y1);
-        }
+        vinv = 1.f / vref;
     };
 
     const uint32_t parity0 = parity;
@@ -542,7 +560,6 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
             }
             float mx0 = fmaxf(fmaxf(scA[0], scA[2]), fmaxf(scB[0], scB[2]));
             float mx1 = fmaxf(fmaxf(scA[1], scA[3]), fmaxf(scB[1], scB[3]));
-            float al0 = 1.f, al1 = 1.f;
             // The reference m need not be the maximum, only so near it that 2^(s - m + 14) fits fp16 (below 2^16):
             // it moves when a logit passes it by more than 1, rarely after a few pages.  (NaN logits never do;
             // their sums are NaN.)
@@ -553,8 +570,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
                 }
                 const float m0 = fmaxf(m_run[0], mx0), m1 = fmaxf(m_run[1], mx1);
-                al0 = exp2_approx(m_run[0] - m0);
-                al1 = exp2_approx(m_run[1] - m1);
+                const float al0 = exp2_approx(m_run[0] - m0), al1 = exp2_approx(m_run[1] - m1);
                 m_run[0] = m0;
                 m_run[1] = m1;
                 l_run[0] *= al0;
@@ -573,19 +589,24 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
                                  exp2_approx(scA[3] + u1)};
             const float pb[4] = {exp2_approx(scB[0] + u0), exp2_approx(scB[1] + u1), exp2_approx(scB[2] + u0),
                                  exp2_approx(scB[3] + u1)};
-            if (p.mode == kModeDelta) page_partials(pa, pb, mn0, mn1, al0, al1, lpA, lpB);
-            uint32_t ptA[kTwo ? 4 : 2], ptB[kTwo ? 4 : 2];
-            round_p(pa, ptA, l_run[0], l_run[1]);
-            round_p(pb, ptB, l_run[0], l_run[1]);
-            if (wA == vref && wB == vref) {     // mostly: powers of two of similar blocks
+            l_run[0] += (pa[0] + pa[2]) + (pb[0] + pb[2]);
+            l_run[1] += (pa[1] + pa[3]) + (pb[1] + pb[3]);
+            if (p.mode == kModeDelta) page_partials(pa, pb, mn0, mn1, lpA, lpB);
+            // A page's V scale in units of the accumulators' goes into its probabilities: a power of two, so p keeps
+            // its 11 bits (down to 2^-18 of the largest at the smallest weight).
+            const float rA = wA * vinv, rB = wB * vinv;
+            if (rA <= 1.f && rA >= 9.5367431640625e-7f && rB <= 1.f && rB >= 9.5367431640625e-7f) {
+                uint32_t ptA[kTwo ? 4 : 2], ptB[kTwo ? 4 : 2];
+                round_p(pa, rA, ptA);
+                round_p(pb, rB, ptB);
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     pv_tile(pA, c, ptA, acc[2 * c], acc[2 * c + 1]);
                     pv_tile(pB, c, ptB, acc[2 * c], acc[2 * c + 1]);
                 }
             } else {
-                pv_rescaled(pA, ptA, wA);
-                pv_rescaled(pB, ptB, wB);
+                pv_rescaled(pA, pa, wA);
+                pv_rescaled(pB, pb, wB);
             }
         }
         __syncwarp();
@@ -610,7 +631,6 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], o);
-            dl_run[j] += __shfl_xor_sync(0xffffffffu, dl_run[j], o);
         }
     }
 #pragma unroll
@@ -622,7 +642,6 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     constexpr int kRow = D + 4;
     float* po = reinterpret_cast<float*>(wst);           // [8][D + 4] outputs
     float* pml = po + kMaxGroup * kRow;                   // [8][2] (max, sum)
-    float* pdl = pml + kMaxGroup * 2;                     // [8][2] delta-layers: over the unrounded terms
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) {
         const int d = mt * 16 + 2 * g4;
@@ -634,8 +653,6 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         for (int j = 0; j < 2; ++j) {
             pml[(2 * t4 + j) * 2] = m_run[j];
             pml[(2 * t4 + j) * 2 + 1] = l_run[j] * kUnshift;
-            pdl[(2 * t4 + j) * 2] = m_run[j];
-            pdl[(2 * t4 + j) * 2 + 1] = dl_run[j] * kUnshift;
         }
     }
     __syncthreads();
@@ -644,8 +661,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     float pre[2][G];   // delta-layers: this CTA's page terms, loaded before the merge
     if (p.fuse_select) select_preload<WARPS * 32, G>(p, b, g, ex.N, pre);
     merge_epilogue<T, D, G, WARPS, WARPS * 32, kRow>(
-        p, smem, mo0, mo0 + kMaxGroup * kRow, recv, b, g, kPart, kPart,
-        (p.mode == kModeDelta) ? mo0 + kMaxGroup * kRow + kMaxGroup * 2 : nullptr);
+        p, smem, mo0, mo0 + kMaxGroup * kRow, recv, b, g, kPart, kPart);
     if (p.fuse_select) select_tail<WARPS * 32, G, D>(p, smem, S::kStages, recv, b, g, ex.n, ex.N, pre);
 }
 
