@@ -30,7 +30,8 @@
  *   tensor-map encoder, the address of delta_full_attn_noalloc's scratch array),
  *   guarded by a mutex; a device reset (cudaDeviceReset) invalidates them, so
  *   reload the library after one.
- * - `stream` is a cudaStream_t passed as void* (NULL = the legacy default stream).
+ * - `stream` is a cudaStream_t passed as void* (NULL = the legacy default stream).  It and every
+ *   device pointer belong to the current device.
  *   Every call only enqueues work: none synchronises the host, so every call can
  *   be captured in a CUDA graph.  Outputs are valid once the stream reaches them.
  * - Element type: DELTA_F32 (IEEE float) or DELTA_BF16 (bfloat16) for q, k, v, o;
@@ -125,7 +126,8 @@ typedef struct {
 
 /* Bytes of workspace any attention call below needs for this shape on the current
  * device.  The workspace is scratch owned by the caller; it must be 256-byte
- * aligned and zero-filled once (delta_workspace_init) before first use. */
+ * aligned and zero-filled once (delta_workspace_init) before first use.  Calls that may overlap on the
+ * GPU (other streams, graphs replayed side by side) need a workspace each. */
 size_t delta_workspace_size(const delta_desc* desc, int32_t batch, int32_t max_pages_per_seq);
 
 /* Workspace for delta_select_attn with the given head reduction: DELTA_HEAD_MAX also keeps
@@ -254,7 +256,7 @@ typedef enum { DELTA_ROPE_HALF = 0, DELTA_ROPE_INTERLEAVED = 1 } delta_rope_layo
 typedef enum { DELTA_ROPE_PLAIN = 0, DELTA_ROPE_LINEAR = 1, DELTA_ROPE_BANDS = 2 } delta_rope_scaling;
 
 typedef struct {
-    int32_t rotary_dim;       /* even, >= 2 */
+    int32_t rotary_dim;       /* even, 2..4096 */
     int32_t scaling;          /* delta_rope_scaling */
     double  base;             /* > 1 */
     double  factor;           /* >= 1; LINEAR and BANDS */
@@ -323,7 +325,7 @@ delta_status delta_kv_append_layers_q8(const delta_desc* desc, const delta_page_
  * token_indptr[b] tokens of each sequence, positions kv_len[b] - m_b .. kv_len[b] - 1, from rows
  * token_indptr[b] + i of k and v ([tokens][num_kv_heads][head_dim] in desc's dtype; row_stride elements from
  * row to row, a multiple of 16 bytes, 0 = contiguous).  token_indptr [batch+1] is device memory; max_tokens
- * is the host's bound on m_b (it sizes the launch; a larger m_b is written all the same).  A page must
+ * is the host's bound on m_b (it sizes the launch; a larger m_b is written all the same; 0: no launch).  A page must
  * belong to one sequence only while it is written.  Slots past the last token are left as they were, tokens before position 0
  * and pages outside the table or the pool are skipped. */
 delta_status delta_kv_write_q8(const delta_desc* desc, const delta_page_table* pt, const int32_t* token_indptr,

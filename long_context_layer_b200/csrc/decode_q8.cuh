@@ -435,10 +435,14 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
             }
             if (!ok0) sc[0] = sc[1] = -INFINITY;
             if (!ok1) sc[2] = sc[3] = -INFINITY;
-            // slots past the end may hold e4m3's NaN: their V rows become zeros
-            const int tv = min(ex.n - t0, kPage);
+            // slots past the end and hidden tokens may hold e4m3's NaN: their V rows become zeros
+            int lo = 0, hi = 0;
+            if (p.mode == kModeWindow) window_gap(p, ex, lp, lo, hi);
             uint4* vz = reinterpret_cast<uint4*>(wst + size_t(s) * S::kPage2 + S::kBlock);
-            for (int i = tv * (D / 16) + lane; i < kPage * (D / 16); i += 32) vz[i] = make_uint4(0, 0, 0, 0);
+            for (int i = lane; i < kPage * (D / 16); i += 32) {
+                const int r = i / (D / 16);
+                if (t0 + r >= ex.n || (r >= lo && r < hi)) vz[i] = make_uint4(0, 0, 0, 0);
+            }
             __syncwarp();
             if (lane == 0) fence_proxy_async_smem();    // ahead of the copy that reuses the stage
         }

@@ -258,6 +258,76 @@ def test_window_reads_no_hidden_page():
     c.check(lambda b, n: seen[b])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_hidden_tokens_may_hold_nan_payloads(dtype):
+    # e4m3's NaN code in every token of the listed pages that the window does not show
+    c = Case("e4m3", dtype, 4, 2, 64, [200, 43], seed=17)
+    k0, v0 = c.pool.numbers("k"), c.pool.numbers("v")
+    for b, n in enumerate(c.lens):
+        seen = set(R.visible(n, 37, 5))
+        for j in sorted({t // PAGE for t in seen}):
+            for s in range(PAGE):
+                if j * PAGE + s not in seen:
+                    c.pool.k[c.paged.phys(b, j), :, s] = 0x7f
+                    c.pool.v[c.paged.phys(b, j), :, s] = 0xff
+    c.L.window_attn_q8(c.desc, c.pt, 37, 5, c.q, c.pool.cache, c.o, c.ws, c.bytes, stream())
+    c._num = {"k": k0, "v": v0}
+    c.check(lambda b, n: R.visible(n, 37, 5))
+
+
+def test_stale_selection_is_replaced_after_the_wait():
+    # the kernel guesses that the selection buffer already holds this call's selection: buffers that hold another,
+    # a shorter, a longer and a garbage list when the launch before it (a delta-layer) writes the real one
+    c = Case("int8", "bf16", 4, 2, 128, [3000, 700, 90], seed=18)
+    L, sp = c.L, c.L.DeltaSelectParams(20, 16, 64, c.L.DELTA_HEAD_SUM)
+    stride = L.sel_capacity(sp)
+    cnt0 = torch.zeros(3, dtype=torch.int32, device="cuda")
+    sel0 = torch.zeros(3, stride, dtype=torch.int32, device="cuda")
+    st = stream()
+    L.select_attn_q8(c.desc, c.pt, sp, c.q, c.pool.cache, c.o, cnt0, sel0, stride, None, c.ws, c.bytes, st)
+    torch.cuda.synchronize()          # the settled entry's own condition
+    L.sparse_attn_settled_q8(c.desc, c.pt, cnt0, sel0, stride, c.q, c.pool.cache, c.o, c.ws, c.bytes, st)
+    want = c.o.clone()
+    other = torch.empty_like(c.o)
+    for cnt_was, sel_was in ((1, 0), (stride, 3), (0, 7), (-5, -1), (2 ** 30, 2 ** 30), (7, 1)):
+        for _ in range(3):
+            cnt = torch.full_like(cnt0, cnt_was)
+            sel = torch.full_like(sel0, sel_was)
+            torch.cuda.synchronize()
+            L.select_attn_q8(c.desc, c.pt, sp, c.q, c.pool.cache, other, cnt, sel, stride, None, c.ws, c.bytes, st)
+            L.sparse_attn_q8(c.desc, c.pt, cnt, sel, stride, c.q, c.pool.cache, c.o, c.ws, c.bytes, st)
+            assert torch.equal(c.o, want), (cnt_was, sel_was)
+            assert torch.equal(cnt, cnt0)
+    assert flags(c.ws) == 0
+
+
+def test_write_then_attention_at_once():
+    # attention launched right behind the bulk write reads the pages it wrote (over and over, other values each time)
+    L = lib()
+    hkv, d, n = 4, 128, 4000
+    paged = Paged([n, n - 7], seed=19)
+    pool = Pool8(paged.pages, hkv, d, "int8")
+    dd = desc(4 * hkv, hkv, d, "bf16", paged.pages)
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    q = torch.randn(2, 4 * hkv, d, generator=gen, device="cuda").bfloat16()
+    rows = torch.tensor([0, n, 2 * n - 7], dtype=torch.int32, device="cuda")
+    nb = L.workspace_size_q8(dd, 2, paged.longest)
+    ws = workspace(nb)
+    xs = [[torch.randn(2 * n - 7, hkv, d, generator=gen, device="cuda").bfloat16() for _ in "kv"] for _ in range(4)]
+    outs, alone = [], []
+    for quiet in (True, False):
+        for i in range(12):
+            o = torch.empty_like(q)
+            k, v = xs[i % 4]
+            L.kv_write_q8(dd, paged.table(), rows, n, k, v, pool.cache, stream=stream())
+            if quiet:
+                torch.cuda.synchronize()
+            L.full_attn_q8(dd, paged.table(), q, pool.cache, o, ws, nb, stream())
+            (alone if quiet else outs).append(o)
+    for a, b in zip(alone, outs):
+        assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     # pools whose pages lie behind 2^32 bytes
     L = lib()
