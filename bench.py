@@ -104,15 +104,16 @@ def run_profile(args):
 
 # ---------------------------------------------------------------------------- helpers
 def kernel_source_hash() -> str:
-    """sha256 over the CUDA sources of the library (identifies the kernels a profile was taken on)."""
+    """sha256 over the CUDA sources of the profiled kernels (full, delta and sparse layers over the bf16 and
+    fp32 caches): identifies the kernels a profile was taken on."""
     import hashlib
     d = os.path.join(ROOT, "long_context_layer_b200", "csrc")
     h = hashlib.sha256()
-    for f in sorted(os.listdir(d)):
-        if f.endswith((".cu", ".cuh", ".h")):
-            h.update(f.encode())
-            with open(os.path.join(d, f), "rb") as fh:
-                h.update(fh.read())
+    for f in sorted(("delta_attn.cu", "common.cuh", "decode_mma.cuh", "decode_simt.cuh", "host.cuh", "launch_plain.cuh",
+                     "select.cuh", "select_tail.cuh")):
+        h.update(f.encode())
+        with open(os.path.join(d, f), "rb") as fh:
+            h.update(fh.read())
     return h.hexdigest()
 
 

@@ -1,4 +1,4 @@
-// Shared device helpers of the DELTA decode kernels (included by delta_attn.cu only).
+// Shared device helpers of the decode kernels.
 #pragma once
 
 #include <cooperative_groups.h>

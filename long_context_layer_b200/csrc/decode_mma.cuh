@@ -1,4 +1,4 @@
-// Tensor-core split-KV decode kernel for bf16 storage (included by delta_attn.cu only).
+// Tensor-core split-KV decode kernel for bf16 storage.
 //
 // One CTA = (split, KV head, sequence); each of its WARPS warps (4, 6 or 8) streams whole pages.  A page of one
 // KV head (16 tokens x D) of K and of V arrives in the warp's shared-memory stage through 2-D

@@ -1,4 +1,4 @@
-// CUDA-core split-KV decode kernel (fp32 storage; included by delta_attn.cu only).
+// CUDA-core split-KV decode kernel (fp32 storage).
 #pragma once
 
 #include "common.cuh"

@@ -1,4 +1,6 @@
-// DELTA decode attention stack for B200 (sm_100a): kernels and the C ABI of include/delta_attn.h.
+// DELTA decode attention stack for B200 (sm_100a): the full, delta and sparse layers over the bf16 / fp32
+// cache, the appends and the calibration calls of include/delta_attn.h.  (Window layers: window_attn.cu; the
+// 8-bit cache: cache_q8.cu and attn_q8.cu; rotary positions: rope.cu.)
 //
 // Method: "DELTA: Dynamic Layer-Aware Token Attention for Efficient Long-Context Reasoning",
 // ai.info summary, section "Methodology in Plain English".  Initial layers run full attention,
