@@ -1,4 +1,5 @@
-"""ctypes binding of include/delta_attn.h (argument marshalling only).
+"""Binding of include/delta_attn.h (argument marshalling only): ctypes, and for the calls of the smallest
+layers the module _fastcall, which does the same with less time a call.
 
 Every function takes device pointers as integers or torch CUDA tensors and passes
 them unchanged to the C ABI; all computation happens in libdelta_attn.so.  Importing
@@ -18,6 +19,11 @@ if not os.path.exists(LIB_PATH):
         "(there is no fallback implementation)")
 
 lib = ctypes.CDLL(LIB_PATH)
+
+try:
+    from ._fastcall import bind as _bind
+except ImportError as e:
+    raise ImportError(f"_fastcall.so is missing: build it with `python -m long_context_layer_b200.build` ({e})") from e
 
 DELTA_OK, DELTA_ERR_INVALID_ARG, DELTA_ERR_UNSUPPORTED, DELTA_ERR_WORKSPACE, DELTA_ERR_CUDA, DELTA_ERR_BOUNDS = range(6)
 DELTA_F32, DELTA_BF16 = 0, 1
@@ -121,7 +127,7 @@ for _name, _args in {
     "delta_sparse_attn_q8": [_D, _PT, _vp, _vp, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
     "delta_sparse_attn_settled_q8": [_D, _PT, _vp, _vp, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
     "delta_window_attn_q8": [_D, _PT, _i32, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
-}.items():
+}.items():      # for callers of lib itself; the functions below call through _fastcall
     getattr(lib, _name).argtypes = _args
     getattr(lib, _name).restype = _i32
 lib.delta_workspace_size_q8.argtypes = [_D, _i32, _i32, _i32]
@@ -249,12 +255,39 @@ def read_device_error(workspace, stream: int = 0) -> tuple:
     return s, flags.value
 
 
+# ------------------------------------------------------------------ calls through _fastcall
+# "p" takes None, an int or a tensor; a structure is passed as it is.
+def _fast(name: str, *kinds):
+    return _bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value, kinds)
+
+
+def _done(status: int, where: str, check: bool) -> int:
+    if status != DELTA_OK and check:
+        raise DeltaError(status, where)
+    return status
+
+
+_ATTN = (DeltaDesc, DeltaPageTable)
+_OUT = ("p", "p", "q", "p")        # o, workspace, its bytes, stream
+_window_attn = _fast("delta_window_attn", *_ATTN, "i", "i", "p", "p", "p", *_OUT)
+_rope = _fast("delta_rope", DeltaDesc, DeltaRope, "q", "p", "q", "p", "q", "p", "q", "p", "q", "p")
+_kv_append_q8 = _fast("delta_kv_append_q8", *_ATTN, "p", "p", DeltaQ8Cache, "p")
+_kv_append_layers_q8 = _fast("delta_kv_append_layers_q8", *_ATTN, "i", "p", "p", "p", "p")
+_kv_write_q8 = _fast("delta_kv_write_q8", *_ATTN, "p", "i", "p", "p", "q", DeltaQ8Cache, "p")
+_kv_read_q8 = _fast("delta_kv_read_q8", *_ATTN, "p", "i", "p", DeltaQ8Cache, "p", "p", "p")
+_full_attn_q8 = _fast("delta_full_attn_q8", *_ATTN, "p", DeltaQ8Cache, *_OUT)
+_select_attn_q8 = _fast("delta_select_attn_q8", *_ATTN, DeltaSelectParams, "p", DeltaQ8Cache, "p", "p", "p", "i", "p",
+                        "p", "q", "p")
+_sparse_attn_q8 = _fast("delta_sparse_attn_q8", *_ATTN, "p", "p", "i", "p", DeltaQ8Cache, *_OUT)
+_sparse_attn_settled_q8 = _fast("delta_sparse_attn_settled_q8", *_ATTN, "p", "p", "i", "p", DeltaQ8Cache, *_OUT)
+_window_attn_q8 = _fast("delta_window_attn_q8", *_ATTN, "i", "i", "p", DeltaQ8Cache, *_OUT)
+
+
 # ------------------------------------------------------------------ window layers
 def window_attn(desc, pt, window_tokens: int, sink_tokens: int, q, k_pool, v_pool, o, workspace, ws_bytes: int,
                 stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_window_attn(ctypes.byref(desc), ctypes.byref(pt), window_tokens, sink_tokens, ptr(q), ptr(k_pool),
-                              ptr(v_pool), ptr(o), ptr(workspace), ws_bytes, stream)
-    return _check(s, "delta_window_attn") if check else s
+    return _done(_window_attn(desc, pt, window_tokens, sink_tokens, q, k_pool, v_pool, o, workspace, ws_bytes, stream),
+                 "delta_window_attn", check)
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -267,9 +300,8 @@ def rope_table(params: DeltaRopeParams) -> list:
 
 def rope(desc, plan: DeltaRope, rows: int, q, q_out, k, k_out, q_stride: int = 0, q_out_stride: int = 0,
          k_stride: int = 0, k_out_stride: int = 0, stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_rope(ctypes.byref(desc), ctypes.byref(plan), rows, ptr(q), q_stride, ptr(q_out), q_out_stride, ptr(k),
-                       k_stride, ptr(k_out), k_out_stride, stream)
-    return _check(s, "delta_rope") if check else s
+    return _done(_rope(desc, plan, rows, q, q_stride, q_out, q_out_stride, k, k_stride, k_out, k_out_stride, stream),
+                 "delta_rope", check)
 
 
 # ------------------------------------------------------------------ the cache held in 8 bits
@@ -278,63 +310,54 @@ def workspace_size_q8(desc, batch: int, max_pages_per_seq: int, reduce: int = DE
 
 
 def kv_append_q8(desc, pt, k_new, v_new, cache: DeltaQ8Cache, stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_kv_append_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(k_new), ptr(v_new), ctypes.byref(cache), stream)
-    return _check(s, "delta_kv_append_q8") if check else s
+    return _done(_kv_append_q8(desc, pt, k_new, v_new, cache, stream), "delta_kv_append_q8", check)
 
 
 def kv_append_layers_q8(desc, pt, k_new, v_new, caches, stream: int = 0, check: bool = True) -> int:
     """k_new, v_new: one tensor or pointer per layer; caches: one DeltaQ8Cache per layer."""
     n = len(caches)
-    s = lib.delta_kv_append_layers_q8(ctypes.byref(desc), ctypes.byref(pt), n, _ptr_array([k_new[l] for l in range(n)]),
-                                      _ptr_array([v_new[l] for l in range(n)]), (DeltaQ8Cache * n)(*caches), stream)
-    return _check(s, "delta_kv_append_layers_q8") if check else s
+    ks, vs = _ptr_array([k_new[l] for l in range(n)]), _ptr_array([v_new[l] for l in range(n)])
+    cs = (DeltaQ8Cache * n)(*caches)
+    return _done(_kv_append_layers_q8(desc, pt, n, ctypes.addressof(ks), ctypes.addressof(vs), ctypes.addressof(cs), stream),
+                 "delta_kv_append_layers_q8", check)
 
 
 def kv_write_q8(desc, pt, token_indptr, max_tokens: int, k, v, cache: DeltaQ8Cache, row_stride: int = 0,
                 stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_kv_write_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(token_indptr), max_tokens, ptr(k), ptr(v),
-                              row_stride, ctypes.byref(cache), stream)
-    return _check(s, "delta_kv_write_q8") if check else s
+    return _done(_kv_write_q8(desc, pt, token_indptr, max_tokens, k, v, row_stride, cache, stream), "delta_kv_write_q8",
+                 check)
 
 
 def kv_read_q8(desc, pt, token_indptr, max_tokens: int, token_start, cache: DeltaQ8Cache, k_out, v_out,
                stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_kv_read_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(token_indptr), max_tokens, ptr(token_start),
-                             ctypes.byref(cache), ptr(k_out), ptr(v_out), stream)
-    return _check(s, "delta_kv_read_q8") if check else s
+    return _done(_kv_read_q8(desc, pt, token_indptr, max_tokens, token_start, cache, k_out, v_out, stream),
+                 "delta_kv_read_q8", check)
 
 
 def full_attn_q8(desc, pt, q, cache: DeltaQ8Cache, o, workspace, ws_bytes: int, stream: int = 0,
                  check: bool = True) -> int:
-    s = lib.delta_full_attn_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(q), ctypes.byref(cache), ptr(o), ptr(workspace),
-                               ws_bytes, stream)
-    return _check(s, "delta_full_attn_q8") if check else s
+    return _done(_full_attn_q8(desc, pt, q, cache, o, workspace, ws_bytes, stream), "delta_full_attn_q8", check)
 
 
 def select_attn_q8(desc, pt, sp, q, cache: DeltaQ8Cache, o, sel_cnt, sel_pages, sel_stride: int, page_scores, workspace,
                    ws_bytes: int, stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_select_attn_q8(ctypes.byref(desc), ctypes.byref(pt), ctypes.byref(sp), ptr(q), ctypes.byref(cache),
-                                 ptr(o), ptr(sel_cnt), ptr(sel_pages), sel_stride, ptr(page_scores), ptr(workspace),
-                                 ws_bytes, stream)
-    return _check(s, "delta_select_attn_q8") if check else s
+    return _done(_select_attn_q8(desc, pt, sp, q, cache, o, sel_cnt, sel_pages, sel_stride, page_scores, workspace,
+                                 ws_bytes, stream), "delta_select_attn_q8", check)
 
 
 def sparse_attn_q8(desc, pt, sel_cnt, sel_pages, sel_stride: int, q, cache: DeltaQ8Cache, o, workspace, ws_bytes: int,
                    stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_sparse_attn_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(sel_cnt), ptr(sel_pages), sel_stride, ptr(q),
-                                 ctypes.byref(cache), ptr(o), ptr(workspace), ws_bytes, stream)
-    return _check(s, "delta_sparse_attn_q8") if check else s
+    return _done(_sparse_attn_q8(desc, pt, sel_cnt, sel_pages, sel_stride, q, cache, o, workspace, ws_bytes, stream),
+                 "delta_sparse_attn_q8", check)
 
 
 def sparse_attn_settled_q8(desc, pt, sel_cnt, sel_pages, sel_stride: int, q, cache: DeltaQ8Cache, o, workspace,
                            ws_bytes: int, stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_sparse_attn_settled_q8(ctypes.byref(desc), ctypes.byref(pt), ptr(sel_cnt), ptr(sel_pages), sel_stride,
-                                         ptr(q), ctypes.byref(cache), ptr(o), ptr(workspace), ws_bytes, stream)
-    return _check(s, "delta_sparse_attn_settled_q8") if check else s
+    return _done(_sparse_attn_settled_q8(desc, pt, sel_cnt, sel_pages, sel_stride, q, cache, o, workspace, ws_bytes,
+                                         stream), "delta_sparse_attn_settled_q8", check)
 
 
 def window_attn_q8(desc, pt, window_tokens: int, sink_tokens: int, q, cache: DeltaQ8Cache, o, workspace, ws_bytes: int,
                    stream: int = 0, check: bool = True) -> int:
-    s = lib.delta_window_attn_q8(ctypes.byref(desc), ctypes.byref(pt), window_tokens, sink_tokens, ptr(q),
-                                 ctypes.byref(cache), ptr(o), ptr(workspace), ws_bytes, stream)
-    return _check(s, "delta_window_attn_q8") if check else s
+    return _done(_window_attn_q8(desc, pt, window_tokens, sink_tokens, q, cache, o, workspace, ws_bytes, stream),
+                 "delta_window_attn_q8", check)

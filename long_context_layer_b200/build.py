@@ -5,8 +5,9 @@
 (Run it by path: importing the package loads the library this script builds.)
 
 Produces long_context_layer_b200/libdelta_attn.so (the C ABI of include/delta_attn.h),
-synth/libsynth_fill.so (the device-side input generator used by tests and the benchmark) and
-synth/libsynth_host.so (the same generator on the host, for fast oracle inputs).
+long_context_layer_b200/_fastcall.so (the binding's call module), synth/libsynth_fill.so (the device-side
+input generator used by tests and the benchmark) and synth/libsynth_host.so (the same generator on the
+host, for fast oracle inputs).
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -31,9 +33,11 @@ TARGETS = [
     ([os.path.join(ROOT, "synth", "csrc", "synth_fill.cu")],
      os.path.join(ROOT, "synth", "libsynth_fill.so"), []),
 ]
-# host (CPU) libraries built with gcc: the input generator's host copy
+# host (CPU) libraries built with gcc: the input generator's host copy and the binding's call module
 HOST_TARGETS = [
-    (os.path.join(ROOT, "synth", "csrc", "synth_host.c"), os.path.join(ROOT, "synth", "libsynth_host.so")),
+    (os.path.join(ROOT, "synth", "csrc", "synth_host.c"), os.path.join(ROOT, "synth", "libsynth_host.so"), []),
+    (os.path.join(CSRC, "fastcall.c"), os.path.join(ROOT, "long_context_layer_b200", "_fastcall.so"),
+     ["-I" + sysconfig.get_paths()["include"]]),
 ]
 
 
@@ -62,10 +66,10 @@ def build(force: bool = False, verbose: bool = False) -> list:
                 list(pool.map(lambda c: subprocess.run(c, check=True), cmds))
             subprocess.run(link, check=True)
         built.append(out)
-    for src, out in HOST_TARGETS:
+    for src, out, extra in HOST_TARGETS:
         if not force and os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(src):
             continue
-        cmd = ["gcc", "-O3", "-ffp-contract=off", "-fno-fast-math", "-fPIC", "-shared", src, "-o", out]
+        cmd = ["gcc", "-O3", "-ffp-contract=off", "-fno-fast-math", "-fPIC", "-shared"] + extra + [src, "-o", out]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         subprocess.run(cmd, check=True)
