@@ -10,10 +10,10 @@
 
 namespace delta {
 
-// Bulk calls run one-warp blocks: a block of 8 warps (8 heads of a page) waits for its slowest, 79 instead of
-// 65 us for the write of 4 x 16k tokens of 8 heads (6.2 TB/s; the read back 71 us, 5.7 TB/s).  A warp of a long
-// write takes 4 consecutive pages, whose table entries it looks up at once (one page a warp: 72 us with two
-// warps a block, against 69).
+// Bulk calls run one-warp blocks: a block of more waits for its slowest warp.  The write of 4 x 16k tokens of 8
+// heads takes 65 us (6.2 TB/s; 69 with 2 or 4 warps a block), the read back 71 us (5.7 TB/s; 74).  A warp of a long
+// write takes 4 consecutive pages, whose table entries it looks up at once (with two warps a block 69 us, two
+// pages a warp 72).  The largest magnitude is taken from the raw bits, two halfwords at a time: 79 -> 69 us.
 constexpr int kMaxColumns = 16384;   // grid columns; more pages are strided over
 constexpr int kWarpsPerSm = 64;      // warps an SM gets before a warp takes more than one page
 constexpr int kMaxChunk = 4;

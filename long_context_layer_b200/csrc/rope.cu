@@ -4,159 +4,166 @@
 // it is formed in double precision and reduced to a fraction of a turn before it is rounded to float; what
 // is left is at most half a turn, whose sine and cosine are accurate to a few float ulps at any position.
 //
-// Bound: HBM, one read and one write of the rows (arithmetic: 3 flops a value and one sine and cosine per
-// (row, pair), shared by all heads of the row through shared memory).
+// Bound: HBM, one read and one write of the rows.  A warp takes a row (or a share of its heads, when there are few
+// rows): it forms the row's sines and cosines once, each lane keeps those of the 16 bytes of a head that it
+// turns, and then streams heads, four groups in flight.  In the half layout a value's partner lies
+// rotary_dim/2 dimensions away, in another lane's 16 bytes (at any offset: widths need not divide): the group
+// passes through shared memory, which also makes in-place safe, a group being read whole before it is written.
 
 #include "host.cuh"
+#include "q8.cuh"
 
 namespace delta {
 
-constexpr int kRopeThreads = 256;
-// Rows a block takes when there are many, and vectors a thread has in flight: 8 and 4 rotate 32,768 rows of 32 +
-// 8 heads of 128 (671 MB moved) in 105 us, 6.4 TB/s; 4 rows 131 us, 2 vectors 127 us, both without the
-// streaming loads and stores, which gave 124 -> 105 us.
-constexpr int kRopeRows = 8;
+// Four groups of heads (512 bytes each) in flight a warp, four blocks an SM (64 registers).  16,384 rows of 32 + 8
+// heads of 128 in bf16 (336 MB moved): adjacent pairs 58 us, 5.8 TB/s, at any width; halves 65 us (5.1 TB/s), 76 us
+// where the partner's offset is no multiple of 16 bytes; fp32 108 and 112 us (6.2 TB/s).  Two groups 73 us (halves),
+// three blocks an SM 70 us; partners by shuffles instead of shared memory 66 and 80 us.
+constexpr int kRopeWarps = 8;
 constexpr int kRopeBatch = 4;
 
 struct RopeParams {
     const double* turns;
     const int32_t* positions;
-    int32_t num_positions, offset, rotary_dim, head_dim;
+    int32_t num_positions, offset, rotary_dim;
     float magnitude;
     int64_t rows;
+    int32_t split;                // warps a row is shared by: 1, 2, 4 or 8
     const void* x[2];             // q, k
     void* y[2];
     int64_t xs[2], ys[2];         // row strides in elements
     int32_t heads[2];
-    uint32_t magic[2];            // ceil(2^32 / heads): i / heads = i * magic >> 32 for i * heads < 2^32
 };
 
-template <typename T, int V>
-struct __align__(sizeof(T) * V) RopeVec {
-    T v[V];
-};
-
-// Rows are read once and written once: evict-first in the caches.
-template <typename Vec>
-__device__ __forceinline__ Vec rope_load(const void* p) {
-    if constexpr (sizeof(Vec) == 16) {
-        const uint4 w = __ldcs(static_cast<const uint4*>(p));
-        return *reinterpret_cast<const Vec*>(&w);
-    } else {
-        return *static_cast<const Vec*>(p);
-    }
+__device__ __forceinline__ uint32_t rope_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
-template <typename Vec>
-__device__ __forceinline__ void rope_store(void* p, const Vec& v) {
-    if constexpr (sizeof(Vec) == 16) __stcs(static_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
-    else *static_cast<Vec*>(p) = v;
+__device__ __forceinline__ uint4 pack16(const float (&x)[8]) {
+    uint4 w;
+    w.x = rope_bf16x2(x[0], x[1]);
+    w.y = rope_bf16x2(x[2], x[3]);
+    w.z = rope_bf16x2(x[4], x[5]);
+    w.w = rope_bf16x2(x[6], x[7]);
+    return w;
+}
+__device__ __forceinline__ uint4 pack16(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
-// A head's work items: `rot` vectors of pairs (V pairs in two vectors rotary_dim/2 apart, HALF; V / 2 adjacent
-// pairs; one pair where V is 1: odd widths), then, unless in place, vectors that pass through.  A thread keeps
-// one item u and walks over the (row, head) list, kRopeBatch of them in flight.
-template <typename T, bool HALF, int V>
-__device__ __forceinline__ void rope_rows(const RopeParams& p, const float2 (*cs)[64], const T* x, T* y, int64_t xs,
-                                          int64_t ys, int heads, uint32_t magic, int64_t r0, int nr) {
-    using Vec = RopeVec<T, V>;
-    const int pairs = p.rotary_dim / 2;
-    const int rot = HALF ? pairs / V : (V == 1 ? pairs : p.rotary_dim / V);
-    const int items = rot + (x == y ? 0 : (p.head_dim - p.rotary_dim) / V);
-    if (items == 0) return;
-    const int slots = kRopeThreads / items, n = nr * heads;      // items <= head_dim <= 128
-    const int slot = threadIdx.x / items, u = threadIdx.x - slot * items;
-    if (slot >= slots) return;
-    const bool pass = u >= rot;
-    // offsets of the item's one or two vectors
-    const int d0 = pass ? p.rotary_dim + (u - rot) * V : HALF || V > 1 ? u * V : 2 * u;
-    const int d1 = HALF ? d0 + pairs : d0 + 1;
-    constexpr bool kSecond = HALF || V == 1;
-    for (int i0 = slot; i0 < n; i0 += kRopeBatch * slots) {
-        Vec a[kRopeBatch], b[kSecond ? kRopeBatch : 1];
-        int row[kRopeBatch], head[kRopeBatch];
-#pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
-            const int i = i0 + k * slots;
-            row[k] = heads == 1 ? i : int(__umulhi(uint32_t(i), magic));
-            head[k] = i - row[k] * heads;
-            if (i >= n) continue;
-            const T* src = x + (r0 + row[k]) * xs + head[k] * p.head_dim;
-            a[k] = rope_load<Vec>(src + d0);
-            if constexpr (kSecond) {
-                if (!pass) b[k] = rope_load<Vec>(src + d1);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
-            if (i0 + k * slots >= n) continue;
-            T* dst = y + (r0 + row[k]) * ys + head[k] * p.head_dim;
-            if (!pass) {
-                const float2* t = cs[row[k]] + (HALF || V == 1 ? u * V : u * V / 2);
-                if constexpr (kSecond) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float fa = Elem<T>::to_f(a[k].v[j]), fb = Elem<T>::to_f(b[k].v[j]);
-                        a[k].v[j] = Elem<T>::from_f(fa * t[j].x - fb * t[j].y);
-                        b[k].v[j] = Elem<T>::from_f(fb * t[j].x + fa * t[j].y);
-                    }
-                    rope_store(dst + d1, b[k]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        const float fa = Elem<T>::to_f(a[k].v[j]), fb = Elem<T>::to_f(a[k].v[j + 1]);
-                        a[k].v[j] = Elem<T>::from_f(fa * t[j / 2].x - fb * t[j / 2].y);
-                        a[k].v[j + 1] = Elem<T>::from_f(fb * t[j / 2].x + fa * t[j / 2].y);
-                    }
-                }
-            }
-            rope_store(dst + d0, a[k]);
-        }
-    }
-}
-
-// One block: the (cos, sin) * magnitude of its rows' pairs, then the rows' heads.
-template <typename T, bool HALF, int V>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int rows_per_block) {
-    __shared__ __align__(16) float2 cs[kRopeRows][64];
-    const int pairs = p.rotary_dim / 2;
-    const int64_t r0 = int64_t(blockIdx.x) * rows_per_block;
-    const int nr = int(min(int64_t(rows_per_block), p.rows - r0));
-    // the table is set up once by the caller; positions may be another kernel's output
+template <typename T, int D, bool HALF>
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const RopeParams p) {
+    constexpr int V = Raw16<T>::N, U = D / V, HP = 32 / U;   // values a lane, lanes a head, heads a group
+    constexpr int TV = HALF ? V : V / 2;                     // sines and cosines a lane
+    __shared__ float2 table[kRopeWarps][D / 2];
+    __shared__ uint4 swap[HALF ? kRopeWarps : 1][kRopeBatch][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t at = int64_t(blockIdx.x) * kRopeWarps + warp;
+    const int64_t row = at / p.split;
+    const int part = int(at - row * p.split);
+    const int rd = p.rotary_dim, pairs = rd / 2;
+    // the table of turns is set up once by the caller; positions may be another kernel's output
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = threadIdx.x; i < nr * pairs; i += kRopeThreads) {
-        const int r = i / pairs, j = i - r * pairs;
-        const int64_t row = r0 + r;
-        const int32_t at = row < p.num_positions ? int32_t(row) : int32_t(row % p.num_positions);
-        const int64_t pos = int64_t(p.positions[at]) + p.offset;
-        const double t = double(pos) * p.turns[j];
-        float s, c;
-        sincospif(2.0f * float(t - rint(t)), &s, &c);
-        cs[r][j] = make_float2(c * p.magnitude, s * p.magnitude);
+    if (row >= p.rows) return;
+    {
+        const int64_t pos = int64_t(p.positions[row < p.num_positions ? row : row % p.num_positions]) + p.offset;
+        for (int j = lane; j < pairs; j += 32) {
+            const double t = double(pos) * p.turns[j];
+            float s, c;
+            sincospif(2.0f * float(t - rint(t)), &s, &c);
+            table[warp][j] = make_float2(c * p.magnitude, s * p.magnitude);
+        }
+        __syncwarp();
     }
-    __syncthreads();
-    if (p.x[0] != nullptr)
-        rope_rows<T, HALF, V>(p, cs, static_cast<const T*>(p.x[0]), static_cast<T*>(p.y[0]), p.xs[0], p.ys[0], p.heads[0],
-                              p.magic[0], r0, nr);
-    if (p.x[1] != nullptr)
-        rope_rows<T, HALF, V>(p, cs, static_cast<const T*>(p.x[1]), static_cast<T*>(p.y[1]), p.xs[1], p.ys[1], p.heads[1],
-                              p.magic[1], r0, nr);
+    const int sub = lane / U, u = lane % U, d0 = u * V;      // the lane's head in a group and its dimensions
+    const bool turned = d0 < rd;                             // (some of them)
+    float cs[TV], sn[TV];
+#pragma unroll
+    for (int i = 0; i < TV; ++i) {
+        const int d = HALF ? d0 + i : d0 + 2 * i;
+        const bool first = d < pairs;
+        const int j = HALF ? (first ? d : d - pairs) : d / 2;
+        // a value that passes through is x * 1 + 0 * -0: itself, its sign of zero too
+        const float2 t = d < rd ? table[warp][j] : make_float2(1.f, -0.f);
+        cs[i] = t.x;
+        sn[i] = HALF && d < rd && first ? -t.y : t.y;
+    }
+    const bool whole = HALF && pairs % V == 0;      // a lane's partners are one other lane's values
+    const int lane2 = sub * U + (!turned ? u : (d0 < pairs ? d0 + pairs : d0 - pairs) / V);
+    const int groups_q = p.x[0] == nullptr ? 0 : (p.heads[0] + HP - 1) / HP;
+    const int groups = groups_q + (p.x[1] == nullptr ? 0 : (p.heads[1] + HP - 1) / HP);
+    const bool pass_q = p.x[0] != p.y[0], pass_k = p.x[1] != p.y[1];     // out of place: the rest is copied
+    for (int g0 = part; g0 < groups; g0 += p.split * kRopeBatch) {
+        uint4 raw[kRopeBatch];
+        uint32_t live = 0;
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k) {
+            const int g = g0 + k * p.split;
+            const bool is_k = g >= groups_q;
+            const int head = (is_k ? g - groups_q : g) * HP + sub;
+            raw[k] = make_uint4(0, 0, 0, 0);
+            if (g < groups && head < (is_k ? p.heads[1] : p.heads[0]) && (turned || (is_k ? pass_k : pass_q))) {
+                const T* x = static_cast<const T*>(is_k ? p.x[1] : p.x[0]) + row * (is_k ? p.xs[1] : p.xs[0]);
+                raw[k] = __ldcs(reinterpret_cast<const uint4*>(x + head * D + d0));
+                live |= 1u << k;
+            }
+        }
+        if constexpr (HALF) {
+#pragma unroll
+            for (int k = 0; k < kRopeBatch; ++k) swap[warp][k][lane] = raw[k];
+            __syncwarp();
+        }
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k) {
+            if (!((live >> k) & 1u)) continue;
+            uint4 out = raw[k];
+            if (turned) {
+                float x[V], r[V];
+                Raw16<T>::get(out, x);
+                if constexpr (HALF) {
+                    float other[V];
+                    if (whole) {
+                        Raw16<T>::get(swap[warp][k][lane2], other);
+                    } else {
+                        const T* head = reinterpret_cast<const T*>(&swap[warp][k][sub * U]);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const int d = d0 + i;
+                            other[i] = d < rd ? Elem<T>::to_f(head[d < pairs ? d + pairs : d - pairs]) : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < V; ++i) r[i] = fmaf(x[i], cs[i], other[i] * sn[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; i += 2) {
+                        const bool in = d0 + i < rd;
+                        r[i] = in ? x[i] * cs[i / 2] - x[i + 1] * sn[i / 2] : x[i];
+                        r[i + 1] = in ? x[i + 1] * cs[i / 2] + x[i] * sn[i / 2] : x[i + 1];
+                    }
+                }
+                out = pack16(r);
+            }
+            const int g = g0 + k * p.split;
+            const bool is_k = g >= groups_q;
+            const int head = (is_k ? g - groups_q : g) * HP + sub;
+            T* y = static_cast<T*>(is_k ? p.y[1] : p.y[0]) + row * (is_k ? p.ys[1] : p.ys[0]);
+            __stcs(reinterpret_cast<uint4*>(y + head * D + d0), out);
+        }
+        if constexpr (HALF) __syncwarp();      // the next groups overwrite the swapped ones
+    }
 }
 
-template <typename T>
-delta_status launch_rope(const RopeParams& p, bool half, cudaStream_t st) {
-    constexpr int V = 16 / int(sizeof(T));
-    const int rd = p.rotary_dim;
-    const bool wide = half ? (rd / 2) % V == 0 : rd % V == 0;   // every vector whole (head_dim is a multiple of V)
-    const int rows = p.rows >= int64_t(device_sm_count()) * 8 * kRopeRows ? kRopeRows : 1;
-    const int64_t blocks = (p.rows + rows - 1) / rows;
+template <typename T, int D>
+delta_status launch_rope(RopeParams p, bool half, cudaStream_t st) {
+    p.split = 1;
+    while (p.split < 8 && p.rows * p.split * 2 <= int64_t(device_sm_count()) * 32) p.split *= 2;
+    const int64_t blocks = (p.rows * p.split + kRopeWarps - 1) / kRopeWarps;
     if (blocks > INT32_MAX) return DELTA_ERR_UNSUPPORTED;
-    const dim3 grid{unsigned(blocks)}, block{kRopeThreads};
-    if (half)
-        return wide ? launch_pdl(rope_kernel<T, true, V>, grid, block, 0, st, p, rows)
-                    : launch_pdl(rope_kernel<T, true, 1>, grid, block, 0, st, p, rows);
-    return wide ? launch_pdl(rope_kernel<T, false, V>, grid, block, 0, st, p, rows)
-                : launch_pdl(rope_kernel<T, false, 1>, grid, block, 0, st, p, rows);
+    const dim3 grid{unsigned(blocks)}, block{kRopeWarps * 32};
+    return half ? launch_pdl(rope_kernel<T, D, true>, grid, block, 0, st, p)
+                : launch_pdl(rope_kernel<T, D, false>, grid, block, 0, st, p);
 }
 
 }  // namespace delta
@@ -213,7 +220,6 @@ delta_status delta_rope(const delta_desc* desc, const delta_rope_plan* rope, int
     const int64_t xs[2] = {q_stride, k_stride}, ys[2] = {q_out_stride, k_out_stride};
     for (int i = 0; i < 2; ++i) {
         const int64_t row = int64_t(p.heads[i]) * desc->head_dim;
-        p.magic[i] = uint32_t((0x100000000ull + p.heads[i] - 1) / p.heads[i]);
         p.xs[i] = xs[i] == 0 ? row : xs[i];
         p.ys[i] = ys[i] == 0 ? row : ys[i];
         if (p.x[i] == nullptr) continue;
@@ -229,12 +235,13 @@ delta_status delta_rope(const delta_desc* desc, const delta_rope_plan* rope, int
     p.num_positions = rope->num_positions;
     p.offset = rope->offset;
     p.rotary_dim = rope->rotary_dim;
-    p.head_dim = desc->head_dim;
     p.magnitude = rope->magnitude;
     p.rows = rows;
     const bool half = rope->layout == DELTA_ROPE_HALF;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return desc->dtype == DELTA_BF16 ? launch_rope<__nv_bfloat16>(p, half, st) : launch_rope<float>(p, half, st);
+    if (desc->dtype == DELTA_BF16)
+        return desc->head_dim == 128 ? launch_rope<__nv_bfloat16, 128>(p, half, st) : launch_rope<__nv_bfloat16, 64>(p, half, st);
+    return desc->head_dim == 128 ? launch_rope<float, 128>(p, half, st) : launch_rope<float, 64>(p, half, st);
 }
 
 }  // extern "C"

@@ -97,3 +97,36 @@ def test_rope_of_many_rows_matches_row_by_row():
     for r in list(range(0, rows, 997)) + [rows - 3, rows - 2, rows - 1]:
         L.rope(d, plan(L, turns, 128, "half", 1.0, pos[r:r + 1], 0), 1, q[r], q1[r], k[r], k1[r], stream=stream())
         assert torch.equal(qo[r], q1[r]) and torch.equal(ko[r], k1[r])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype,rd", [("bf16", 50), ("bf16", 6), ("f32", 62), ("bf16", 64)])
+def test_other_dimensions_pass_through_whatever_they_hold(dtype, rd, layout):
+    L = lib()
+    x = make(3, 4, 128, dtype, 7).view(3, 4, 128)
+    odd = torch.tensor([float("inf"), -float("inf"), -0.0, 0.0, float("nan")], device="cuda").to(x.dtype)
+    x[..., rd:] = odd.repeat(26)[: 128 - rd]
+    turns = torch.from_numpy(R.rope_turns(rd)).cuda()
+    pos = torch.tensor([5, 90, 7], dtype=torch.int32, device="cuda")
+    out = torch.full_like(x, 3.0)
+    L.rope(desc(4, 4, 128, dtype, 0), plan(L, turns, rd, layout, 1.0, pos, 0), 3, x, out, None, None, stream=stream())
+    a, b = out[..., rd:], x[..., rd:]
+    assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(9.0), b.nan_to_num(9.0))
+    assert torch.equal(torch.signbit(a) & ~a.isnan(), torch.signbit(b) & ~b.isnan())
+    assert bool(out[..., :rd].isfinite().all())
+
+
+@pytest.mark.parametrize("rows", [2, 600, 1300, 2600, 5000])
+def test_every_split_of_rows_over_warps(rows):
+    L = lib()
+    turns_h = R.rope_turns(30)
+    turns = torch.from_numpy(turns_h).cuda()
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda") * 3
+    q, k = make(rows, 5, 64, "f32", 8), make(rows, 5, 64, "f32", 9)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    L.rope(desc(5, 5, 64, "f32", 0), plan(L, turns, 30, "half", 1.0, pos, 0), rows, q, qo, k, ko, stream=stream())
+    pick = sorted({0, 1, rows // 3, rows - 2, rows - 1})
+    for x0, out in ((q, qo), (k, ko)):
+        x = host(x0)[pick].reshape(len(pick), 5, 64)
+        ref = R.rope(x, [3 * r for r in pick], turns_h, "half")
+        assert_within(host(out)[pick].reshape(len(pick), 5, 64), ref, tolerance(x, ref, turns_h, "half", 1.0, "f32"))
