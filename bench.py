@@ -104,13 +104,12 @@ def run_profile(args):
 
 # ---------------------------------------------------------------------------- helpers
 def kernel_source_hash() -> str:
-    """sha256 over the CUDA sources of the profiled kernels (full, delta and sparse layers over the bf16 and
+    """sha256 over the device sources of the profiled kernels (full, delta and sparse layers over the bf16 and
     fp32 caches): identifies the kernels a profile was taken on."""
     import hashlib
     d = os.path.join(ROOT, "long_context_layer_b200", "csrc")
     h = hashlib.sha256()
-    for f in sorted(("delta_attn.cu", "common.cuh", "decode_mma.cuh", "decode_simt.cuh", "host.cuh", "launch_plain.cuh",
-                     "select.cuh", "select_tail.cuh")):
+    for f in ("common.cuh", "decode_mma.cuh", "decode_simt.cuh", "delta_attn.cu", "select.cuh", "select_tail.cuh"):
         h.update(f.encode())
         with open(os.path.join(d, f), "rb") as fh:
             h.update(fh.read())

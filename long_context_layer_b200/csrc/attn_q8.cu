@@ -69,7 +69,7 @@ struct Q8Cache {
             *threads = k.threads;
             return k.fn;
         };
-        return fit_plan(plan_q8(dtype, D, batch, Hkv, items), kernel_of, batch * Hkv, items, fused);
+        return fit_plan(plan_q8(dtype, D, batch, Hkv, items), kernel_of, batch * Hkv, items, fused, 1);
     }
     void fill(DecodeParams& prm) const {
         prm.k_pool = c->k_pool;

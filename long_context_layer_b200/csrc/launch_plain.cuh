@@ -289,7 +289,8 @@ struct PlainCache {
             *threads = dtype == DELTA_BF16 ? variant_threads(variant) : kThreads;
             return decode_ptr<WIN>(dtype, D, G, variant, smem);
         };
-        return fit_plan(plan_splits(dtype, D, batch, Hkv, items, fused), kernel_of, batch * Hkv, items, fused);
+        return fit_plan(plan_splits(dtype, D, batch, Hkv, items, fused), kernel_of, batch * Hkv, items, fused,
+                        WIN ? 1 : 0);
     }
     void fill(DecodeParams& prm) const {
         prm.k_pool = k_pool;
