@@ -10,9 +10,11 @@
 //        and 4 t4 + {2, 3} of a 16-byte chunk; the product sums over dimensions, so their order is free as long
 //        as Q's fragments follow it.  (The 8-bit mma.m16n8k32 over e4m3 operands is executed as two fp16
 //        products with conversions of both operands: 115 instead of 104 us for the delta-layer of 16 x 16k.)
-//        int8: the payload is an operand of mma.m16n8k32 over bytes, and a query is 16-bit fixed point, high
-//        bytes (signed) and low bytes (unsigned) on two integer accumulators: exact down to 2^-7 of the head's
-//        largest element, the others to 2^-15 of it.  No conversion of K (85 instead of 91 us for 4 x 64k).
+//        int8: the payload is an operand of mma.m16n8k32 over bytes, and a query is 23-bit fixed point, its high
+//        bytes (signed), middle and low bytes (unsigned) on three integer accumulators: exact down to 2^-14 of
+//        the head's largest element, the others to 2^-22 of it.  No conversion of K (84 us for 4 x 64k,
+//        91 in fp16).  Two bytes would do for even queries and save 2 to 6 % where lists are short, but leave
+//        2^-15 of the largest element, which queries with an outlying dimension would show.
 //        fp32 queries: the fp16 form with a query as the sum of two values (22 bits and the sign).
 //   s = S * (Q's factor per head) * (K's block scale): powers of two and the softmax scale, in fp32.
 //   online softmax as in decode_mma.cuh, with p = 2^(s - m + 14) so that fp16 holds small probabilities
@@ -303,8 +305,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     }
 
     // ---- Q^T fragments of head g4: dimensions 16 kk + 4 t4 + {0, 1, 2, 3} are this lane's
-    constexpr int kTop = 14;    // the largest element is scaled into [2^14, 2^15)
-    uint32_t qa[KS], qc[KS], qx[kTwo ? KS : 1], qy[kTwo ? KS : 1];
+    constexpr int kTop = kHalf ? 14 : 21;    // the largest element is scaled into [2^kTop, 2^(kTop + 1))
+    constexpr bool kThree = !kHalf;          // 24-bit fixed point in three bytes: qa, qc, qx
+    uint32_t qa[KS], qc[KS], qx[kTwo || kThree ? KS : 1], qy[kTwo ? KS : 1];
     float qf0, qf1;           // factors of this lane's logits (heads 2 t4, 2 t4 + 1)
     {
         // bf16: two registers of two; fp32: four
@@ -359,12 +362,13 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
                     qy[kk] = pack_f16(q[2] - rc.x, q[3] - rc.y);
                 }
             } else {
-                // the nearest integer (within +-2^15 - 128) in the low 16 bits of q + 1.5 * 2^23
+                // the nearest integer, within +-2^22, from the bits of q + 1.5 * 2^23
                 uint32_t i[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) i[j] = __float_as_uint(q[j] + 12582912.f);
-                qa[kk] = __byte_perm(__byte_perm(i[0], i[1], 0x0051), __byte_perm(i[2], i[3], 0x0051), 0x5410);
-                qc[kk] = __byte_perm(__byte_perm(i[0], i[1], 0x0040), __byte_perm(i[2], i[3], 0x0040), 0x5410);
+                for (int j = 0; j < 4; ++j) i[j] = __float_as_uint(q[j] + 12582912.f) - 0x4b400000u;
+                qa[kk] = __byte_perm(__byte_perm(i[0], i[1], 0x0062), __byte_perm(i[2], i[3], 0x0062), 0x5410);
+                qc[kk] = __byte_perm(__byte_perm(i[0], i[1], 0x0051), __byte_perm(i[2], i[3], 0x0051), 0x5410);
+                qx[kk] = __byte_perm(__byte_perm(i[0], i[1], 0x0040), __byte_perm(i[2], i[3], 0x0040), 0x5410);
             }
         }
         qf0 = __shfl_sync(0xffffffffu, factor, 8 * t4);
@@ -392,10 +396,10 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     for (int c = 0; c < CH; ++c) off[c] = uint32_t(row) * D + (((2 * c + sub) ^ swz) << 4);
     const uint32_t st0 = smem_addr(wst);
 
-    // K . Q^T of 32 dimensions of the page in stage s.  c0 and c1: of the chunk's two halves (fp16), or the
-    // products with Q's high and low bytes.
+    // K . Q^T of 32 dimensions of the page in stage s.  c0 and c1: of the chunk's two halves (fp16); or c0, c1, c2:
+    // the products with Q's bytes, high to low.
     using Sum = std::conditional_t<kHalf, float, int>;
-    auto qk_chunk = [&](int s, int c, Sum (&c0)[4], Sum (&c1)[4]) {
+    auto qk_chunk = [&](int s, int c, Sum (&c0)[4], Sum (&c1)[4], Sum (&c2)[4]) {
         uint32_t r[4];
         ldmatrix_x4(st0 + uint32_t(s) * S::kPage2 + off[c], r[0], r[1], r[2], r[3]);
         if constexpr (kHalf) {
@@ -411,19 +415,20 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         } else {
             mma_s8s8_16832(c0, r, qa[2 * c], qa[2 * c + 1]);
             mma_s8u8_16832(c1, r, qc[2 * c], qc[2 * c + 1]);
+            mma_s8u8_16832(c2, r, qx[2 * c], qx[2 * c + 1]);
         }
     };
-    auto sum_of = [](Sum high, Sum low) {
-        if constexpr (std::is_same_v<Sum, int>) return float(high * 256 + low);
-        else return high + low;
+    auto sum_of = [](Sum x, Sum y, Sum z) {
+        if constexpr (std::is_same_v<Sum, int>) return fmaf(float(x), 65536.f, float(y * 256 + z));   // below 2^31 each
+        else return x + y;
     };
     // base-2 logits of a page: tokens g4, g4 + 8, heads 2 t4, 2 t4 + 1
-    auto logits_of = [&](const Sum (&c0)[4], const Sum (&c1)[4], float ks, int lp, int s, float (&sc)[4]) {
+    auto logits_of = [&](const Sum (&c0)[4], const Sum (&c1)[4], const Sum (&c2)[4], float ks, int lp, int s, float (&sc)[4]) {
         const float f0 = qf0 * ks, f1 = qf1 * ks;
-        sc[0] = sum_of(c0[0], c1[0]) * f0;
-        sc[1] = sum_of(c0[1], c1[1]) * f1;
-        sc[2] = sum_of(c0[2], c1[2]) * f0;
-        sc[3] = sum_of(c0[3], c1[3]) * f1;
+        sc[0] = sum_of(c0[0], c1[0], c2[0]) * f0;
+        sc[1] = sum_of(c0[1], c1[1], c2[1]) * f1;
+        sc[2] = sum_of(c0[2], c1[2], c2[2]) * f0;
+        sc[3] = sum_of(c0[3], c1[3], c2[3]) * f1;
         const int t0 = lp * kPage;
         const bool whole = t0 + kPage <= ex.n && (p.mode != kModeWindow || t0 + kPage <= p.sink || t0 >= ex.from);
         if (!whole) {      // the last page, and pages at the edge of the sinks or the window
@@ -547,14 +552,15 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
             const float kA = vA ? ksA : ksB, kB = vB ? ksB : ksA, wA = vA ? vsA : vsB, wB = vB ? vsB : vsA;
             float scA[4], scB[4];
             {
-                Sum a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0}, b0[4] = {0, 0, 0, 0}, b1[4] = {0, 0, 0, 0};
+                Sum a0[4] = {0, 0, 0, 0}, a1[4] = {0, 0, 0, 0}, a2[4] = {0, 0, 0, 0};
+                Sum b0[4] = {0, 0, 0, 0}, b1[4] = {0, 0, 0, 0}, b2[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    qk_chunk(pA, c, a0, a1);
-                    qk_chunk(pB, c, b0, b1);
+                    qk_chunk(pA, c, a0, a1, a2);
+                    qk_chunk(pB, c, b0, b1, b2);
                 }
-                logits_of(a0, a1, kA, vA ? lpA : lpB, pA, scA);
-                logits_of(b0, b1, kB, vB ? lpB : lpA, pB, scB);
+                logits_of(a0, a1, a2, kA, vA ? lpA : lpB, pA, scA);
+                logits_of(b0, b1, b2, kB, vB ? lpB : lpA, pB, scB);
             }
             if (!vA) scA[0] = scA[1] = scA[2] = scA[3] = -INFINITY;
             if (!vB) scB[0] = scB[1] = scB[2] = scB[3] = -INFINITY;

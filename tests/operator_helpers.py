@@ -5,7 +5,7 @@ Attention: with w the weights, an output is sum_t w_t v_t; a relative error d_t 
 normalise) moves it by at most 2 max|d_t| max|v|.  A weight's relative error is ln 2 times the absolute error of
 its base-2 logit plus exp2's (2^-22) plus the rounding of p for the matrix product.  A logit is a sum of D
 products: at most (D + 8) roundings of partial sums no larger than A = max_t sum_i |q_i k_ti| / sqrt(D) * log2 e.
-bf16 queries over the int8 cache are 16-bit fixed point: an element is off by at most Q_PART of the head's largest,
+bf16 queries over the int8 cache are 23-bit fixed point: an element is off by at most Q_PART of the head's largest,
 which moves a logit by at most that times sum_i |k_ti| / sqrt(D) nats (e4m3: fp16, 2^-24 below 2^-14 of 2^14).
 The sum over tokens runs over at most n / 16 + 32 fp32 additions of partial sums no larger than max|v|.
 """
@@ -22,7 +22,7 @@ PAGE = 16
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 HALF_STEP = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 P_ROUND = {"bf16": 2.0 ** -11, "f32": 2.0 ** -22}      # p as one fp16 value, or as the sum of two
-Q_PART = {"e4m3": 2.0 ** -39, "int8": 2.0 ** -15}      # half a step of the smallest unit
+Q_PART = {"e4m3": 2.0 ** -39, "int8": 2.0 ** -22}      # half a step of the smallest unit
 PAYLOAD = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
 
 

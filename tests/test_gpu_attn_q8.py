@@ -87,6 +87,17 @@ def test_blocks_of_very_different_scales(fmt, dtype):
         c.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_queries_with_an_outlying_dimension(fmt, dtype):
+    # one dimension 3000 times the others, which the keys hardly have: the logits hang on the small ones
+    c = Case(fmt, dtype, 4, 2, 128, [500, 90], seed=21)
+    c.q[..., 7] *= 3000
+    c.pool.k[..., 7] = 0
+    c.L.full_attn_q8(c.desc, c.pt, c.q, c.pool.cache, c.o, c.ws, c.bytes, stream())
+    c.check()
+
+
 def test_scales_need_not_be_powers_of_two():
     # a cache written elsewhere with the same layout: any finite scale
     c = Case("int8", "bf16", 4, 2, 128, [300, 65], seed=8)
