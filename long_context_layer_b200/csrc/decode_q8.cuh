@@ -18,8 +18,9 @@
 //        fp32 queries: the fp16 form with a query as the sum of two values (22 bits and the sign).
 //   s = S * (Q's factor per head) * (K's block scale): powers of two and the softmax scale, in fp32.
 //   online softmax as in decode_mma.cuh, with p = 2^(s - m + 14) so that fp16 holds small probabilities
-//        (to 2^-38 of the largest; the offset cancels in o = acc / l).  l sums the fp32 terms, which are also the
-//        page terms of a delta-layer (fp32 outputs: p as the sum of two fp16 values).
+//        (to 2^-38 of the largest; the offset cancels in o = acc / l).  For the product p is the sum of two fp16
+//        values (22 bits and the signs), so that an output is off by its own rounding and what fp32 sums explain.
+//        l sums the fp32 terms, which are also the page terms of a delta-layer.
 //   O^T[D x 8] += V8^T[D x 16] . (V's block scale / unit * P^T)[16 x 8]   ldmatrix.trans moves 2-byte units, that is
 //        two dimensions of one token; a byte permute separates them, and the accumulator's rows g4 and g4 + 8
 //        are dimensions 2 g4 and 2 g4 + 1 of the 16-dimension tile.
@@ -163,10 +164,11 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
                                                                   const __grid_constant__ CUtensorMap tmap_v) {
     using S = Q8Smem<D, STAGES, WARPS>;
     using H = Half8<FMT>;
-    constexpr bool kTwo = sizeof(T) == 4;      // fp32 queries and outputs: fp16 pairs
+    constexpr bool kTwo = sizeof(T) == 4;      // fp32 queries: fp16 pairs
     constexpr bool kHalf = kTwo || FMT == kE4M3;    // QK in fp16, else in 8-bit integers
     constexpr int KS = D / 16;                 // k-steps of the QK product = M-tiles of the PV product
     constexpr int CH = D / 32;                 // ldmatrix.x4 of a block
+    constexpr bool kTwin = G <= 4;             // columns 4..7 of the products are the heads 0..3 once more
     constexpr float kShift = 14.f, kUnshift = 6.103515625e-05f;    // 2^14, 2^-14
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         if (pages.lp_b == newest) q8_scales(p, g, pages.lp_b, pages.ph_b, -1, pages.ks_b, pages.vs_b);
     }
 
-    // ---- Q^T fragments of head g4: dimensions 16 kk + 4 t4 + {0, 1, 2, 3} are this lane's
+    // ---- Q^T fragments of head g4 (kTwin: g4 & 3): dimensions 16 kk + 4 t4 + {0, 1, 2, 3} are this lane's
     constexpr int kTop = kHalf ? 14 : 21;    // the largest element is scaled into [2^kTop, 2^(kTop + 1))
     constexpr bool kThree = !kHalf;          // 24-bit fixed point in three bytes: qa, qc, qx
     uint32_t qa[KS], qc[KS], qx[kTwo || kThree ? KS : 1], qy[kTwo ? KS : 1];
@@ -312,18 +314,19 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     {
         // bf16: two registers of two; fp32: four
         uint32_t raw[KS][kTwo ? 4 : 2];
-        const T* qp = reinterpret_cast<const T*>(p.q) + (size_t(b) * Hq + h0 + g4) * D + 4 * t4;
+        const int hq = kTwin ? g4 & 3 : g4;
+        const T* qp = reinterpret_cast<const T*>(p.q) + (size_t(b) * Hq + h0 + hq) * D + 4 * t4;
         uint32_t amax = 0;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
             if constexpr (kTwo) {
-                const uint4 w = g4 < G ? *reinterpret_cast<const uint4*>(qp + kk * 16) : make_uint4(0, 0, 0, 0);
+                const uint4 w = hq < G ? *reinterpret_cast<const uint4*>(qp + kk * 16) : make_uint4(0, 0, 0, 0);
                 raw[kk][0] = w.x;
                 raw[kk][1] = w.y;
                 raw[kk][2] = w.z;
                 raw[kk][3] = w.w;
             } else {
-                const uint2 w = g4 < G ? *reinterpret_cast<const uint2*>(qp + kk * 16) : make_uint2(0, 0);
+                const uint2 w = hq < G ? *reinterpret_cast<const uint2*>(qp + kk * 16) : make_uint2(0, 0);
                 raw[kk][0] = w.x;
                 raw[kk][1] = w.y;
             }
@@ -476,28 +479,35 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         if (2 * t4 + 1 < G) { lg[(2 * t4 + 1) * hs + g4] = sc[1]; lg[(2 * t4 + 1) * hs + g4 + 8] = sc[3]; }
     };
     // Tile pair c (dimensions 32 c .. 32 c + 31) of V^T . P^T of the page in stage s, added to d0 and d1.
-    auto pv_tile = [&](int s, int c, const uint32_t (&pt)[kTwo ? 4 : 2], float (&d0)[4], float (&d1)[4]) {
+    using Probs = uint32_t[kTwin ? 2 : 4];
+    auto pv_tile = [&](int s, int c, const Probs& pt, float (&d0)[4], float (&d1)[4]) {
         uint32_t r0, r1, r2, r3, a0, a1, a2, a3;
         ldmatrix_x4_trans(st0 + uint32_t(s) * S::kPage2 + S::kBlock + off[c], r0, r1, r2, r3);
         H::apart(r0, a0, a1);
         H::apart(r1, a2, a3);
         mma_f16_16816(d0, a0, a1, a2, a3, pt[0], pt[1]);
-        if constexpr (kTwo) mma_f16_16816(d0, a0, a1, a2, a3, pt[2], pt[3]);
+        if constexpr (!kTwin) mma_f16_16816(d0, a0, a1, a2, a3, pt[2], pt[3]);
         H::apart(r2, a0, a1);
         H::apart(r3, a2, a3);
         mma_f16_16816(d1, a0, a1, a2, a3, pt[0], pt[1]);
-        if constexpr (kTwo) mma_f16_16816(d1, a0, a1, a2, a3, pt[2], pt[3]);
+        if constexpr (!kTwin) mma_f16_16816(d1, a0, a1, a2, a3, pt[2], pt[3]);
     };
-    // the probabilities of a page, times w, as P^T fragments
-    auto round_p = [&](const float (&e)[4], float w, uint32_t (&pt)[kTwo ? 4 : 2]) {
+    // The probabilities of a page, times w, as P^T fragments: the fp16 value and what it leaves, rounded again.  Up to
+    // four heads leave half of the eight columns free: the heads' twins in columns 4..7 carry the second values
+    // through the same products (joined at the end); more heads take a second product.
+    auto round_p = [&](const float (&e)[4], float w, Probs& pt) {
         const float x[4] = {e[0] * w, e[1] * w, e[2] * w, e[3] * w};
         const uint32_t x0 = pack_f16(x[0], x[1]), x1 = pack_f16(x[2], x[3]);
-        pt[0] = movmatrix_trans(x0);
-        pt[1] = movmatrix_trans(x1);
-        if constexpr (kTwo) {
-            const float2 r0 = unpack_f16(x0), r1 = unpack_f16(x1);
-            pt[2] = movmatrix_trans(pack_f16(x[0] - r0.x, x[1] - r0.y));
-            pt[3] = movmatrix_trans(pack_f16(x[2] - r1.x, x[3] - r1.y));
+        const float2 r0 = unpack_f16(x0), r1 = unpack_f16(x1);
+        const uint32_t y0 = pack_f16(x[0] - r0.x, x[1] - r0.y), y1 = pack_f16(x[2] - r1.x, x[3] - r1.y);
+        if constexpr (kTwin) {
+            pt[0] = movmatrix_trans(t4 < 2 ? x0 : y0);
+            pt[1] = movmatrix_trans(t4 < 2 ? x1 : y1);
+        } else {
+            pt[0] = movmatrix_trans(x0);
+            pt[1] = movmatrix_trans(x1);
+            pt[2] = movmatrix_trans(y0);
+            pt[3] = movmatrix_trans(y1);
         }
     };
     // A page whose V scale does not go with the accumulators' unit (the largest scale so far): a larger one, which
@@ -512,7 +522,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
                 for (int j = 0; j < 4; ++j) acc[mt][j] *= r;
         }
         const float w = vs / vref;
-        uint32_t pt[kTwo ? 4 : 2];
+        Probs pt;
         round_p(e, 1.f, pt);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -606,7 +616,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
             // its 11 bits (down to 2^-18 of the largest at the smallest weight).
             const float rA = wA * vinv, rB = wB * vinv;
             if (rA <= 1.f && rA >= 9.5367431640625e-7f && rB <= 1.f && rB >= 9.5367431640625e-7f) {
-                uint32_t ptA[kTwo ? 4 : 2], ptB[kTwo ? 4 : 2];
+                Probs ptA, ptB;
                 round_p(pa, rA, ptA);
                 round_p(pb, rB, ptB);
 #pragma unroll
@@ -636,6 +646,12 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
             mbar_wait(&wbar[k % STAGES], parity0 ^ ((k / STAGES) & 1));
     }
     const float unit = vref * kUnshift;      // of the accumulators
+    if constexpr (kTwin) {
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[mt][j] += __shfl_xor_sync(0xffffffffu, acc[mt][j], 2);
+    }
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
 #pragma unroll
