@@ -384,8 +384,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     float acc[KS][4];
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-    float vref = 1.175494351e-38f;             // unit of acc: the largest V scale so far (from 2^-126)
-    float vinv = 8.507059173e37f;              // 1 / vref
+    // unit of acc: the largest V scale so far, at first of the warp's first 32 pages (from 2^-126; NaN if one is)
+    float vref = __uint_as_float(max(0x00800000u, __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(pages.vs_a)))));
+    float vinv = 1.f / vref;
 
     // ldmatrix roles of this lane: matrix lj = (rows 8 (lj & 1) .. + 7, 16-byte chunk 2 c + (lj >> 1))
     const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
@@ -492,11 +493,11 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         mma_f16_16816(d1, a0, a1, a2, a3, pt[0], pt[1]);
         if constexpr (!kTwin) mma_f16_16816(d1, a0, a1, a2, a3, pt[2], pt[3]);
     };
-    // The probabilities of a page, times w, as P^T fragments: the fp16 value and what it leaves, rounded again.  Up to
+    // The probabilities of a page, weighted, as P^T fragments: the fp16 value and what it leaves, rounded again.  Up to
     // four heads leave half of the eight columns free: the heads' twins in columns 4..7 carry the second values
-    // through the same products (joined at the end); more heads take a second product.
-    auto round_p = [&](const float (&e)[4], float w, Probs& pt) {
-        const float x[4] = {e[0] * w, e[1] * w, e[2] * w, e[3] * w};
+    // through the same products (joined at the end); more heads take a second product.  w0, w1: of heads 2 t4, 2 t4 + 1.
+    auto round_p = [&](const float (&e)[4], float w0, float w1, Probs& pt) {
+        const float x[4] = {e[0] * w0, e[1] * w1, e[2] * w0, e[3] * w1};
         const uint32_t x0 = pack_f16(x[0], x[1]), x1 = pack_f16(x[2], x[3]);
         const float2 r0 = unpack_f16(x0), r1 = unpack_f16(x1);
         const uint32_t y0 = pack_f16(x[0] - r0.x, x[1] - r0.y), y1 = pack_f16(x[2] - r1.x, x[3] - r1.y);
@@ -511,30 +512,40 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
         }
     };
     // A page whose V scale does not go with the accumulators' unit (the largest scale so far): a larger one, which
-    // becomes the unit, or one below 2^-20 of it (or NaN), whose product is scaled in fp32.
+    // becomes the unit, or one below 2^-6 of it (or NaN).  Its product is scaled in fp32, and the probabilities of each
+    // head by the power of two that brings the page's largest to [2^14, 2^15): they keep 22 bits down to 2^-16 of it,
+    // however small the page's weight is next to the reference (large values may make up for it).
     auto pv_rescaled = [&](int s, const float (&e)[4], float vs) {
         if (!(fabsf(vs) <= vref)) {
             const float r = vref / fabsf(vs);
             vref = fabsf(vs);
+            vinv = 1.f / vref;
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[mt][j] *= r;
         }
-        const float w = vs / vref;
+        float top[2] = {fmaxf(e[0], e[2]), fmaxf(e[1], e[3])}, up[2], down[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+            const uint32_t x = max((__float_as_uint(top[j]) >> 23) & 0xffu, 27u);     // 2^(x - 127) <= top, from 2^-100
+            up[j] = __uint_as_float((127u + 14u + 127u - x) << 23);
+            down[j] = vs / vref * __uint_as_float((x - 14u) << 23);
+        }
         Probs pt;
-        round_p(e, 1.f, pt);
+        round_p(e, up[0], up[1], pt);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
             pv_tile(s, c, pt, d0, d1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                acc[2 * c][j] = fmaf(d0[j], w, acc[2 * c][j]);
-                acc[2 * c + 1][j] = fmaf(d1[j], w, acc[2 * c + 1][j]);
+                acc[2 * c][j] = fmaf(d0[j], down[j & 1], acc[2 * c][j]);
+                acc[2 * c + 1][j] = fmaf(d1[j], down[j & 1], acc[2 * c + 1][j]);
             }
         }
-        vinv = 1.f / vref;
     };
 
     const uint32_t parity0 = parity;
@@ -612,13 +623,15 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
             l_run[0] += (pa[0] + pa[2]) + (pb[0] + pb[2]);
             l_run[1] += (pa[1] + pa[3]) + (pb[1] + pb[3]);
             if (p.mode == kModeDelta) page_partials(pa, pb, mn0, mn1, lpA, lpB);
-            // A page's V scale in units of the accumulators' goes into its probabilities: a power of two, so p keeps
-            // its 11 bits (down to 2^-18 of the largest at the smallest weight).
+            // A page's V scale in the accumulators' unit goes into its probabilities: a power of two of at least 2^-6, so p keeps
+            // 22 bits down to 2^-10 of the largest, and what is lost below (2^-33 of the largest, in the page's own V
+            // scale) adds up to an fp32 rounding over some thousand tokens a warp.
+            constexpr float kFold = 0.015625f;
             const float rA = wA * vinv, rB = wB * vinv;
-            if (rA <= 1.f && rA >= 9.5367431640625e-7f && rB <= 1.f && rB >= 9.5367431640625e-7f) {
+            if (rA <= 1.f && rA >= kFold && rB <= 1.f && rB >= kFold) {
                 Probs ptA, ptB;
-                round_p(pa, rA, ptA);
-                round_p(pb, rB, ptB);
+                round_p(pa, rA, rA, ptA);
+                round_p(pb, rB, rB, ptB);
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     pv_tile(pA, c, ptA, acc[2 * c], acc[2 * c + 1]);
