@@ -177,7 +177,7 @@ class DeltaStack:
             # a sparse layer after a sparse or window layer uses the settled entry: the selection and
             # the appended tokens were final before the previous layer's kernel began its work (it
             # waited on the delta-layer that wrote the selection), so this layer may read them early
-            self._layer(l, kind, cur, q, k_pools, v_pools, out, st)
+            self._layer(l, kind, cur, q, k_pools, v_pools, out, st, l > 0)
             if kind == DELTA:
                 cur = self.delta_layers.index(l)
 
@@ -225,7 +225,9 @@ class DeltaStack:
                 self._append(k_use, v_new_dev, k_pools, v_pools, a, b, st)
             for l in range(a, b):
                 kind = self.kinds[l]
-                self._layer(l, kind, cur, q_use, k_pools, v_pools, out_dev, st)
+                # (the first layer of a group stands behind the group's append and rotation, not behind a layer)
+                self._layer(l, kind, cur, q_use, k_pools, v_pools, out_dev, st,
+                            l > a or (l > 0 and not append and self.rope is None))
                 if kind == DELTA:
                     cur = self.delta_layers.index(l)
                 if l + 1 - c0 == per or l >= L - 2:
@@ -238,7 +240,8 @@ class DeltaStack:
         main.wait_stream(up)
         main.wait_stream(down)
 
-    def _layer(self, l, kind, cur, q, k_pools, v_pools, out, st):
+    def _layer(self, l, kind, cur, q, k_pools, v_pools, out, st, behind_layer):
+        """behind_layer: the launch before this one on the stream is layer l - 1's."""
         d, pt, ws, wb = self.desc, self.pt, self.workspace, self.ws_bytes
         # what the entry points of this cache take in the place of the pools
         pools = (k_pools[l], v_pools[l]) if self.cache is None else (k_pools[l].c,)
@@ -252,7 +255,7 @@ class DeltaStack:
             scores = self.page_scores[c] if self.page_scores is not None else None
             self._select(q[l], pools, out[l], self.sel_cnt[c], self.sel_pages[c], scores, st)
         else:
-            settled = l > 0 and self.kinds[l - 1] in (SPARSE, WINDOW)
+            settled = behind_layer and self.kinds[l - 1] in (SPARSE, WINDOW)
             fn = ((N.sparse_attn_settled_q8 if q8 else N.sparse_attn_settled) if settled
                   else (N.sparse_attn_q8 if q8 else N.sparse_attn))
             fn(d, pt, self.sel_cnt[cur], self.sel_pages[cur], self.sel_stride, q[l], *pools, out[l], ws, wb, st)
