@@ -300,6 +300,9 @@ delta_status delta_rope(const delta_desc* desc, const delta_rope_plan* rope, int
  * own; when the scale grows, the older values are rounded again to the new one.  Growth at least
  * doubles a step, so all roundings of a value together stay below one step of its block's scale.
  * Writing the first slot of a page starts its blocks anew.
+ * Blocks written elsewhere may hold any finite scale >= 0: attention and the read back multiply by it, and tokens
+ * written into such a block keep the larger of it and their own power of two, as above (a value kept at a scale that
+ * is no power of two is x / scale, rounded in fp32 and then to 8 bits).
  * A non-finite value makes its block's scale NaN until the block starts anew (every value of the block
  * then reads as NaN): it shows in the output as it would in an unquantised cache. */
 typedef enum { DELTA_E4M3 = 0, DELTA_INT8 = 1 } delta_q8_format;

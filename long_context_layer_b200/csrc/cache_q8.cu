@@ -57,7 +57,7 @@ __device__ __forceinline__ void store_block(const uint4 (&raw)[Rows<T, D, ROWS>:
     const bool fine = scale_finite(now);
     const float inv = fine ? scale_inverse(now) : 0.f;
     if (f0 > 0 && now != before && fine) {
-        const float ratio = __uint_as_float(before) * inv;      // <= 1/2, a power of two
+        const float ratio = __uint_as_float(before) * inv;      // <= 1/2 and a power of two (a block written elsewhere: < 1)
         for (int i = lane; i < f0 * D / 16; i += 32) {
             uint4* p = reinterpret_cast<uint4*>(block) + i;
             uint4 w = __ldcg(p);

@@ -28,8 +28,13 @@ __device__ __forceinline__ uint32_t block_scale_bits(uint32_t amax) {
     e = max(e, -100);
     return uint32_t(e + 127) << 23;
 }
-// 1 / 2^e of a finite scale (exponent field 27..249).
-__device__ __forceinline__ float scale_inverse(uint32_t bits) { return __uint_as_float((254u << 23) - bits); }
+// 1 / scale of a finite scale > 0.  Exact for the powers of two that block_scale_bits makes; a block written elsewhere
+// may hold any other scale, and then the quotient x / scale is rounded twice in fp32 before its rounding to 8 bits.
+__device__ __forceinline__ float scale_inverse(uint32_t bits) {
+    const uint32_t e = bits >> 23;
+    if ((bits & 0x7fffffu) == 0u && e >= 1u && e <= 252u) return __uint_as_float((254u << 23) - bits);
+    return 1.0f / __uint_as_float(bits);
+}
 __device__ __forceinline__ bool scale_finite(uint32_t bits) { return bits < 0x7f800000u; }
 
 // Two scaled values to two payload bytes (low byte first), rounded to nearest even.
