@@ -126,8 +126,11 @@ typedef struct {
 
 /* Bytes of workspace any attention call below needs for this shape on the current
  * device.  The workspace is scratch owned by the caller; it must be 256-byte
- * aligned and zero-filled once (delta_workspace_init) before first use.  Calls that may overlap on the
- * GPU (other streams, graphs replayed side by side) need a workspace each. */
+ * aligned and zero-filled once (delta_workspace_init) before first use.  It may then serve calls of
+ * any shapes, cache kinds and scoring modes in turn, as long as it is large enough for each and each
+ * is given the same ws_bytes (the workspace's own size: where its parts lie depends on it); with
+ * another ws_bytes initialise it again.  Calls that may overlap on the GPU (other streams, graphs
+ * replayed side by side) need a workspace each. */
 size_t delta_workspace_size(const delta_desc* desc, int32_t batch, int32_t max_pages_per_seq);
 
 /* Workspace for delta_select_attn with the given head reduction: DELTA_HEAD_MAX also keeps

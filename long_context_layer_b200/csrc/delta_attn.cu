@@ -101,7 +101,7 @@ delta_status run_attention(int mode, const delta_desc* d, const delta_page_table
                            const int32_t* sel_cnt_in, const int32_t* sel_pages_in, int32_t sel_stride_in,
                            const void* q, const void* k_pool, const void* v_pool, void* o, int32_t* sel_cnt_out,
                            int32_t* sel_pages_out, int32_t sel_stride_out, float* page_scores, void* ws,
-                           size_t ws_bytes, void* stream, bool settled = false) {
+                           size_t ws_bytes, void* stream, bool settled = false, size_t lead = 0) {
     AttnCall a;
     a.mode = mode;
     a.d = d;
@@ -119,6 +119,7 @@ delta_status run_attention(int mode, const delta_desc* d, const delta_page_table
     a.page_scores = page_scores;
     a.ws = ws;
     a.ws_bytes = ws_bytes;
+    a.lead = lead;
     a.stream = stream;
     return run_attention_on(PlainCache<false>{k_pool, v_pool}, a);
 }
@@ -237,13 +238,13 @@ delta_status delta_full_attn_noalloc(const delta_desc* desc, const delta_page_ta
     if (s != DELTA_OK) return s;
     if (pt->batch == 0) return DELTA_OK;
     const WsLayout L = ws_layout(desc, pt->batch, pt->max_pages_per_seq);
-    if (L.total > kStaticScratchBytes) return DELTA_ERR_UNSUPPORTED;   // shape needs more scratch than the array holds
+    if (L.zeros + L.scratch > kStaticScratchBytes) return DELTA_ERR_UNSUPPORTED;   // shape needs more scratch than the array holds
     unsigned char* ws = noalloc_scratch();
     if (ws == nullptr) return DELTA_ERR_CUDA;
-    // the error word and the split-arrival tickets must start at zero; the rest is overwritten
-    if (cudaMemsetAsync(ws, 0, L.part_ml, static_cast<cudaStream_t>(stream)) != cudaSuccess) return DELTA_ERR_CUDA;
+    // the error word and the split-arrival tickets must start at zero; the rest is unused or overwritten
+    if (cudaMemsetAsync(ws, 0, L.score_acc, static_cast<cudaStream_t>(stream)) != cudaSuccess) return DELTA_ERR_CUDA;
     return run_attention(kModeFull, desc, pt, nullptr, nullptr, nullptr, 0, q, k_pool, v_pool, o, nullptr, nullptr, 0,
-                         nullptr, ws, kStaticScratchBytes, stream);
+                         nullptr, ws, kStaticScratchBytes, stream, false, L.zeros);
 }
 
 delta_status delta_select_attn(const delta_desc* desc, const delta_page_table* pt, const delta_select_params* sp,

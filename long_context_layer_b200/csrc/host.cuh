@@ -15,10 +15,18 @@
 
 namespace delta {
 
+// A workspace is two areas: the counters and accumulators that every launch leaves at zero, from its start, and scratch,
+// from workspace_lead(its bytes) on.  The lead depends on the workspace's size alone, so calls of any shapes that share
+// one never put scratch where another's counters are.
 struct WsLayout {
-    size_t err, tickets, seq_tickets, part_ml, part_o, page_lse, split_ml, score_acc, keys, logits,
-        total;
+    size_t err, tickets, seq_tickets, score_acc, zeros;                      // from the start; bytes of the area
+    size_t part_ml, part_o, page_lse, split_ml, keys, logits, scratch;       // from the lead; bytes of the area
+    size_t total;                                                            // the smallest workspace that holds both
 };
+
+// (A 32nd: a page has 8 bytes of accumulators, and 4 (heads + 1) of scratch, 68 a head more for HEAD_MAX.)
+constexpr size_t kLeadPart = 32;
+inline size_t workspace_lead(size_t ws_bytes) { return ws_bytes / kLeadPart & ~size_t(255); }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -55,19 +63,32 @@ inline int device_sm_count() {
 inline WsLayout ws_layout_splits(const delta_desc* d, int batch, int max_pages, int S, bool with_logits) {
     WsLayout w{};
     const size_t rows = size_t(batch) * d->num_q_heads;
+    const size_t pages = size_t(batch) * size_t(max_pages);
     size_t off = 0;
-    // the counters (error word, tickets) come first: they are the part that must start at zero
-    w.err = off;          off += align256(64);
-    w.tickets = off;      off += align256(size_t(batch) * d->num_kv_heads * sizeof(int));
-    w.seq_tickets = off;  off += align256(size_t(batch) * sizeof(int));
-    w.part_ml = off;      off += align256(rows * S * sizeof(float2));
-    w.part_o = off;       off += align256(rows * S * d->head_dim * sizeof(float));
-    w.page_lse = off;     off += align256(rows * size_t(max_pages) * sizeof(float));
-    w.split_ml = off;     off += align256(rows * S * sizeof(float2));
-    w.score_acc = off;    off += align256(size_t(batch) * size_t(max_pages) * sizeof(unsigned long long));
-    w.keys = off;         off += align256(size_t(batch) * size_t(max_pages) * sizeof(uint32_t));
-    w.logits = off;       off += with_logits ? align256(rows * size_t(max_pages) * kPage * sizeof(float)) : 0;
-    w.total = off;
+    auto area = [&](size_t bytes) {
+        const size_t at = off;
+        off += align256(bytes);
+        return at;
+    };
+    w.err = area(64);
+    w.tickets = area(size_t(batch) * d->num_kv_heads * sizeof(int));
+    w.seq_tickets = area(size_t(batch) * sizeof(int));
+    w.score_acc = area(pages * sizeof(unsigned long long));
+    w.zeros = off;
+    off = 0;
+    w.part_ml = area(rows * S * sizeof(float2));
+    w.part_o = area(rows * S * d->head_dim * sizeof(float));
+    w.page_lse = area(rows * size_t(max_pages) * sizeof(float));
+    w.split_ml = area(rows * S * sizeof(float2));
+    w.keys = area(pages * sizeof(uint32_t));
+    const size_t logits = align256(rows * size_t(max_pages) * kPage * sizeof(float));
+    // Without the logits the total leaves room for what they move the lead by, so that they add their own bytes only.
+    const size_t for_zeros = kLeadPart * w.zeros;
+    const size_t room = off + logits / kLeadPart;
+    const size_t for_scratch = align256(room + room / (kLeadPart - 1) + 1);
+    w.total = (for_zeros > for_scratch ? for_zeros : for_scratch) + (with_logits ? logits : 0);
+    w.logits = area(with_logits ? logits : 0);
+    w.scratch = off;
     return w;
 }
 
@@ -344,6 +365,7 @@ struct AttnCall {
     float* page_scores = nullptr;
     void* ws = nullptr;
     size_t ws_bytes = 0;
+    size_t lead = 0;             // of a workspace that one shape alone uses (0: workspace_lead)
     void* stream = nullptr;
 };
 
@@ -388,7 +410,7 @@ delta_status run_attention_on(const Backend& be, const AttnCall& a) {
     if (a.ws == nullptr || (reinterpret_cast<uintptr_t>(a.ws) & 255u) != 0) return DELTA_ERR_WORKSPACE;
     const bool head_max = a.mode == kModeDelta && sp->reduce == DELTA_HEAD_MAX;
     const WsLayout L = be.layout(d, pt->batch, pt->max_pages_per_seq, head_max);
-    if (a.ws_bytes < L.total) return DELTA_ERR_WORKSPACE;
+    if (a.lead == 0 && a.ws_bytes < L.total) return DELTA_ERR_WORKSPACE;
 
     const int D = d->head_dim, Hq = d->num_q_heads, Hkv = d->num_kv_heads;
     int items = pt->max_pages_per_seq;
@@ -403,6 +425,7 @@ delta_status run_attention_on(const Backend& be, const AttnCall& a) {
     if (fused && plan.clusters != 1) return DELTA_ERR_UNSUPPORTED;
     const int S = plan.splits();
     unsigned char* base = static_cast<unsigned char*>(a.ws);
+    unsigned char* scratch = base + (a.lead != 0 ? a.lead : workspace_lead(a.ws_bytes));
 
     DecodeParams prm{};
     prm.q = a.q;
@@ -422,14 +445,14 @@ delta_status run_attention_on(const Backend& be, const AttnCall& a) {
     const float scale = d->sm_scale > 0.f ? d->sm_scale : 1.0f / sqrtf(float(D));
     prm.qscale = scale * 1.4426950408889634f;
     prm.mode = a.mode;
-    prm.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
-    prm.part_o = reinterpret_cast<float*>(base + L.part_o);
-    prm.page_lse = reinterpret_cast<float*>(base + L.page_lse);
-    prm.split_ml = a.mode == kModeDelta ? reinterpret_cast<float2*>(base + L.split_ml) : nullptr;
+    prm.part_ml = reinterpret_cast<float2*>(scratch + L.part_ml);
+    prm.part_o = reinterpret_cast<float*>(scratch + L.part_o);
+    prm.page_lse = reinterpret_cast<float*>(scratch + L.page_lse);
+    prm.split_ml = a.mode == kModeDelta ? reinterpret_cast<float2*>(scratch + L.split_ml) : nullptr;
     prm.err = reinterpret_cast<int*>(base + L.err);
     prm.o = a.o;
     prm.num_clusters = plan.clusters;
-    prm.logits = head_max ? reinterpret_cast<float*>(base + L.logits) : nullptr;
+    prm.logits = head_max ? reinterpret_cast<float*>(scratch + L.logits) : nullptr;
     prm.tickets = reinterpret_cast<int*>(base + L.tickets);
     prm.settled = (a.mode == kModeSparse && a.settled) ? 1 : 0;
     prm.window = a.window;
@@ -445,7 +468,7 @@ delta_status run_attention_on(const Backend& be, const AttnCall& a) {
         prm.sel_stride_out = a.sel_stride_out;
         prm.page_scores = a.page_scores;
         prm.score_acc = reinterpret_cast<unsigned long long*>(base + L.score_acc);
-        prm.keys = reinterpret_cast<uint32_t*>(base + L.keys);
+        prm.keys = reinterpret_cast<uint32_t*>(scratch + L.keys);
         prm.seq_tickets = reinterpret_cast<int*>(base + L.seq_tickets);
     }
     s = be.launch(d, prm, plan, pt->batch, static_cast<cudaStream_t>(a.stream));
