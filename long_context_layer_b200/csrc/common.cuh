@@ -298,6 +298,14 @@ __device__ __forceinline__ void pages_advance(WarpPages& w, const P& p, const Se
     }
 }
 
+// Whether the page table's entry of logical page j of sequence b lies outside the pool (the decode kernels skip such a
+// page and raise kErrPage, so only launches that find that flag need to look).
+template <typename P>
+__device__ __forceinline__ bool bad_entry(const P& p, int b, int j) {
+    const int64_t x = p.indices[p.indptr[b] + j];
+    return x < 0 || x >= p.num_phys_pages;
+}
+
 // Page k of the warp (all lanes call; k must lie in chunk cur or cur + 1).
 __device__ __forceinline__ void pages_get(const WarpPages& w, int k, int& lp, int& ph) {
     const bool a = (k >> 5) == w.cur;

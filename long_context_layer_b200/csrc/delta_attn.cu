@@ -52,6 +52,8 @@ delta_status launch_score_select(const AttnCall& a, const DecodeParams& prm) {
     const int Hq = a.d->num_q_heads;
     SelectParams sp2{};
     sp2.indptr = a.pt->page_indptr;
+    sp2.indices = a.pt->page_indices;
+    sp2.num_phys_pages = a.d->num_phys_pages;
     sp2.kv_len = a.pt->kv_len;
     sp2.page_lse = prm.page_lse;
     sp2.split_ml = prm.split_ml;

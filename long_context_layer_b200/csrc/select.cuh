@@ -8,6 +8,8 @@ namespace delta {
 // ------------------------------------------------------------------ score + select kernel
 struct SelectParams {
     const int32_t* indptr;
+    const int32_t* indices;
+    int64_t num_phys_pages;
     const int32_t* kv_len;
     const float* page_lse;   // [B][Hq][max_pages] log2-sum-exp of each page's base-2 logits
     const float2* split_ml;  // [B][Hq][num_splits] (max, sum) of each decode split
@@ -152,7 +154,9 @@ __global__ void __launch_bounds__(kSelectThreads) score_select_kernel(const Sele
 
     // 2. page scores of this CTA's pages
     uint32_t kmin_loc = 0xffffffffu, kmax_loc = 0u;
+    const bool skipped = (__ldcg(p.err) & kErrPage) != 0;    // some page: those score 0 (their terms are an earlier launch's)
     auto put_key = [&](int j, float sc) {
+        if (skipped && bad_entry(p, b, j)) sc = 0.f;
         const uint32_t key = order_key(sc);
         keys[j - j0] = key;
         if (!forced(j)) {

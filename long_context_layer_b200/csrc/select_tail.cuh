@@ -61,9 +61,10 @@ __device__ __forceinline__ bool arrive_last(int* counter, int expected, uint32_t
 
 // Delta-layers, one cluster per unit: this CTA's page terms lse_hj for its first 2 NTHR pages,
 // loaded right after the loop (its warps wrote them before the preceding block barrier) so that
-// their latency overlaps the output merge.
+// their latency overlaps the output merge.  Returns the workspace's error flags (this CTA's own among them): a
+// skipped page has no terms, what stands there is an earlier launch's.
 template <int NTHR, int G>
-__device__ __forceinline__ void select_preload(const DecodeParams& p, int b, int g, int N, float (&pre)[2][G]) {
+__device__ __forceinline__ int select_preload(const DecodeParams& p, int b, int g, int N, float (&pre)[2][G]) {
     const size_t maxp = size_t(p.max_pages);
     const float* pl = p.page_lse + (size_t(b) * p.num_q_heads + g * G) * maxp;
     const int i0 = blockIdx.x * p.items_per_split, i1 = min(i0 + p.items_per_split, N);
@@ -74,6 +75,7 @@ __device__ __forceinline__ void select_preload(const DecodeParams& p, int b, int
             const int j = i0 + int(threadIdx.x) + i * NTHR;
             pre[i][h] = (j < i1) ? pl[size_t(h) * maxp + j] : -INFINITY;
         }
+    return __ldcg(p.err);
 }
 
 // Steps of the sequence's last CTA: page scores and their order keys, the threshold key T and the
@@ -340,11 +342,11 @@ __device__ __noinline__ void select_final(const SelectFinal a, unsigned char* sm
 
 // Every thread of the CTA calls this after the output merge.  smem: the kernel's page-stage area,
 // idle by now (free_bytes long, 16-byte aligned); recv: the merge's receive area; n, N: the
-// sequence's tokens and pages; pre: select_preload's terms.
+// sequence's tokens and pages; pre, flags: select_preload's terms and flags.
 template <int NTHR, int G, int D>
 __device__ __forceinline__ void select_tail(const DecodeParams& p, unsigned char* smem, size_t free_bytes,
                                             const float* recv, int b, int g, int n, int N,
-                                            const float (&pre)[2][G]) {
+                                            const float (&pre)[2][G], int flags) {
     const int tid = threadIdx.x;
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, S = p.num_splits, h0 = g * G;
     const size_t maxp = size_t(p.max_pages);
@@ -354,6 +356,7 @@ __device__ __forceinline__ void select_tail(const DecodeParams& p, unsigned char
     unsigned long long* acc = p.score_acc + size_t(b) * maxp;
     // adds the unit's share of page j's score (the sum over its G heads of 2^(lse_hj - c_h))
     auto add_share = [&](int j, const float (&v)[G]) {
+        if ((flags & kErrPage) && bad_entry(p, b, j)) return;     // a skipped page scores 0
         float sc = 0.f;
 #pragma unroll
         for (int h = 0; h < G; ++h) sc += exp2_approx(v[h] - s_c[h]);
