@@ -240,13 +240,14 @@ delta_status delta_full_attn_noalloc(const delta_desc* desc, const delta_page_ta
     if (s != DELTA_OK) return s;
     if (pt->batch == 0) return DELTA_OK;
     const WsLayout L = ws_layout(desc, pt->batch, pt->max_pages_per_seq);
-    if (L.zeros + L.scratch > kStaticScratchBytes) return DELTA_ERR_UNSUPPORTED;   // shape needs more scratch than the array holds
+    if (L.counters + L.scratch > kStaticScratchBytes) return DELTA_ERR_UNSUPPORTED;   // shape needs more scratch than the array holds
     unsigned char* ws = noalloc_scratch();
     if (ws == nullptr) return DELTA_ERR_CUDA;
-    // the error word and the split-arrival tickets must start at zero; the rest is unused or overwritten
-    if (cudaMemsetAsync(ws, 0, L.score_acc, static_cast<cudaStream_t>(stream)) != cudaSuccess) return DELTA_ERR_CUDA;
+    // the error word and the split-arrival tickets must start at zero; a full layer has no score accumulators, and the
+    // rest is overwritten
+    if (cudaMemsetAsync(ws, 0, L.counters, static_cast<cudaStream_t>(stream)) != cudaSuccess) return DELTA_ERR_CUDA;
     return run_attention(kModeFull, desc, pt, nullptr, nullptr, nullptr, 0, q, k_pool, v_pool, o, nullptr, nullptr, 0,
-                         nullptr, ws, kStaticScratchBytes, stream, false, L.zeros);
+                         nullptr, ws, kStaticScratchBytes, stream, false, L.counters);
 }
 
 delta_status delta_select_attn(const delta_desc* desc, const delta_page_table* pt, const delta_select_params* sp,
