@@ -25,7 +25,7 @@ SplitPlan plan_q8_variant(int D, int batch, int Hkv, int items, int variant) {
     const bool wide = variant == kVarWide;
     const int warps = q8_warps(D, wide);
     const int slots = device_sm_count() * (wide ? 1 : 2);
-    int s = slots / (batch * Hkv);
+    int s = int(slots / (int64_t(batch) * Hkv));     // (the size function takes any batch)
     const int per_cta = wide ? warps : 2 * warps - 1;
     s = min(s, (items + per_cta - 1) / per_cta);
     s = max(1, min(s, kMaxSplits));

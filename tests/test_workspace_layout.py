@@ -1,4 +1,7 @@
 """CPU: workspace sizes grow with the shape and hold their two areas."""
+import subprocess
+import sys
+
 import pytest
 
 import long_context_layer_b200 as L
@@ -30,3 +33,15 @@ def test_the_logits_add_their_own_bytes(size):
         assert b - a == -(-64 * batch * hq * pages // 256) * 256
         lead = b // 32 // 256 * 256
         assert b - lead >= 68 * batch * hq * pages + 4 * batch * pages
+
+
+def test_the_largest_batches_are_answered():
+    # in a process of its own: a product of batch and heads that came out as 0 in 32 bits ended it
+    code = ("import long_context_layer_b200 as L\n"
+            "for hkv in (64, 16, 4, 1):\n"
+            "    d = L.DeltaDesc(hkv, hkv, 128, 16, L.DELTA_BF16, 0.0, 16)\n"
+            "    sizes = [[f(d, b, 4, r) for b in (1 << 16, 1 << 26, 1 << 27, 1 << 28, 1 << 30, 2 ** 31 - 1)]\n"
+            "             for f in (L.workspace_size_reduce, L.workspace_size_q8) for r in (0, 1)]\n"
+            "    assert all(s == sorted(s) and s[0] > 0 for s in sizes), sizes\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=L.__path__[0] + "/..")
+    assert r.returncode == 0, r.stderr[-500:]
