@@ -25,6 +25,7 @@ from __future__ import annotations
 import argparse
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -104,15 +105,23 @@ def run_profile(args):
 
 # ---------------------------------------------------------------------------- helpers
 def kernel_source_hash() -> str:
-    """sha256 over the device sources of the profiled kernels (full, delta and sparse layers over the bf16 and
-    fp32 caches): identifies the kernels a profile was taken on."""
+    """sha256 over the sources of the profiled kernels (full, delta and sparse layers over the bf16 and fp32 caches):
+    delta_attn.cu and every file of its folder that it includes, directly or not (the kernels, and the split plans and
+    variants that their launches go by).  Identifies the kernels a profile was taken on."""
     import hashlib
     d = os.path.join(ROOT, "long_context_layer_b200", "csrc")
-    h = hashlib.sha256()
-    for f in ("common.cuh", "decode_mma.cuh", "decode_simt.cuh", "delta_attn.cu", "select.cuh", "select_tail.cuh"):
-        h.update(f.encode())
+    texts, todo = {}, ["delta_attn.cu"]
+    while todo:
+        f = todo.pop()
+        if f in texts or not os.path.exists(os.path.join(d, f)):
+            continue
         with open(os.path.join(d, f), "rb") as fh:
-            h.update(fh.read())
+            texts[f] = fh.read()
+        todo += re.findall(r'^\s*#\s*include\s+"([^"]+)"', texts[f].decode(), re.M)
+    h = hashlib.sha256()
+    for f in sorted(texts):
+        h.update(f.encode())
+        h.update(texts[f])
     return h.hexdigest()
 
 
