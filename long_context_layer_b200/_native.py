@@ -8,6 +8,7 @@ this module fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -22,8 +23,8 @@ lib = ctypes.CDLL(LIB_PATH)
 
 try:
     from ._fastcall import bind as _bind
-except ImportError as e:
-    raise ImportError(f"_fastcall.so is missing: build it with `python -m long_context_layer_b200.build` ({e})") from e
+except ImportError:     # not built for this interpreter: the same calls through ctypes, with more time a call
+    _bind = None
 
 DELTA_OK, DELTA_ERR_INVALID_ARG, DELTA_ERR_UNSUPPORTED, DELTA_ERR_WORKSPACE, DELTA_ERR_CUDA, DELTA_ERR_BOUNDS = range(6)
 DELTA_F32, DELTA_BF16 = 0, 1
@@ -127,7 +128,7 @@ for _name, _args in {
     "delta_sparse_attn_q8": [_D, _PT, _vp, _vp, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
     "delta_sparse_attn_settled_q8": [_D, _PT, _vp, _vp, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
     "delta_window_attn_q8": [_D, _PT, _i32, _i32, _vp, _Q8, _vp, _vp, _sz, _vp],
-}.items():      # for callers of lib itself; the functions below call through _fastcall
+}.items():      # for callers of lib itself, and where _fastcall is not built
     getattr(lib, _name).argtypes = _args
     getattr(lib, _name).restype = _i32
 lib.delta_workspace_size_q8.argtypes = [_D, _i32, _i32, _i32]
@@ -256,9 +257,36 @@ def read_device_error(workspace, stream: int = 0) -> tuple:
 
 
 # ------------------------------------------------------------------ calls through _fastcall
-# "p" takes None, an int or a tensor; a structure is passed as it is.
+# "p" takes None, an int or a tensor; "i" and "q" a 32- or 64-bit integer; a structure is passed as it is.
 def _fast(name: str, *kinds):
+    if _bind is None:
+        return _through_ctypes(name, kinds)
     return _bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value, kinds)
+
+
+_RANGE = {"p": (0, 2 ** 64 - 1), "i": (-2 ** 31, 2 ** 31 - 1), "q": (-2 ** 63, 2 ** 63 - 1)}
+
+
+def _through_ctypes(name: str, kinds):
+    """What _fastcall's bind gives, with its conversions and refusals."""
+    types = {"p": ctypes.c_void_p, "i": ctypes.c_int32, "q": ctypes.c_int64}
+    fn = ctypes.CFUNCTYPE(ctypes.c_int32, *[types.get(k, ctypes.c_void_p) for k in kinds])((name, lib))
+
+    def word(kind, x):
+        if not isinstance(kind, str):
+            if type(x) is not kind:
+                raise TypeError(f"expected {kind.__name__}, got {type(x).__name__}")
+            return ctypes.addressof(x)      # the caller holds x during the call
+        x = ptr(x) if kind == "p" else operator.index(x)
+        if x is not None and not _RANGE[kind][0] <= x <= _RANGE[kind][1]:
+            raise OverflowError(f"{x} does not fit the argument")
+        return x
+
+    def call(*args):
+        if len(args) != len(kinds):
+            raise TypeError(f"{name} takes {len(kinds)} positional arguments")
+        return fn(*[word(k, x) for k, x in zip(kinds, args)])
+    return call
 
 
 def _done(status: int, where: str, check: bool) -> int:

@@ -5,9 +5,9 @@
 (Run it by path: importing the package loads the library this script builds.)
 
 Produces long_context_layer_b200/libdelta_attn.so (the C ABI of include/delta_attn.h),
-long_context_layer_b200/_fastcall.so (the binding's call module), synth/libsynth_fill.so (the device-side
-input generator used by tests and the benchmark) and synth/libsynth_host.so (the same generator on the
-host, for fast oracle inputs).
+long_context_layer_b200/_fastcall.<tag>.so (the binding's call module, named for the interpreter it is built for
+and left out where Python's headers are missing), synth/libsynth_fill.so (the device-side input generator used by
+tests and the benchmark) and synth/libsynth_host.so (the same generator on the host, for fast oracle inputs).
 """
 from __future__ import annotations
 
@@ -36,9 +36,11 @@ TARGETS = [
 # host (CPU) libraries built with gcc: the input generator's host copy and the binding's call module
 HOST_TARGETS = [
     (os.path.join(ROOT, "synth", "csrc", "synth_host.c"), os.path.join(ROOT, "synth", "libsynth_host.so"), []),
-    (os.path.join(CSRC, "fastcall.c"), os.path.join(ROOT, "long_context_layer_b200", "_fastcall.so"),
-     ["-I" + sysconfig.get_paths()["include"]]),
 ]
+PACKAGE = os.path.join(ROOT, "long_context_layer_b200")
+PYTHON_INCLUDE = sysconfig.get_paths()["include"]
+FASTCALL = (os.path.join(CSRC, "fastcall.c"), os.path.join(PACKAGE, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX")),
+            ["-I" + PYTHON_INCLUDE])
 
 
 def nvcc() -> str:
@@ -66,7 +68,15 @@ def build(force: bool = False, verbose: bool = False) -> list:
                 list(pool.map(lambda c: subprocess.run(c, check=True), cmds))
             subprocess.run(link, check=True)
         built.append(out)
-    for src, out, extra in HOST_TARGETS:
+    host = list(HOST_TARGETS)
+    if os.path.exists(os.path.join(PYTHON_INCLUDE, "Python.h")):
+        host.append(FASTCALL)
+    elif verbose:
+        print("Python.h is missing: the binding calls through ctypes", file=sys.stderr)
+    untagged = os.path.join(PACKAGE, "_fastcall.so")     # an earlier build's, which any interpreter would load
+    if os.path.exists(untagged):
+        os.remove(untagged)
+    for src, out, extra in host:
         if not force and os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(src):
             continue
         cmd = ["gcc", "-O3", "-ffp-contract=off", "-fno-fast-math", "-fPIC", "-shared"] + extra + [src, "-o", out]
