@@ -37,7 +37,8 @@ class Q8Pools:
         if format not in FORMATS:
             raise ValueError(f"format must be one of {sorted(FORMATS)}")
         self.format = format
-        self.k = torch.zeros(num_phys_pages, num_kv_heads, 16, head_dim, dtype=torch.uint8, device=device)
+        self.shape = (num_phys_pages, num_kv_heads, 16, head_dim)
+        self.k = torch.zeros(self.shape, dtype=torch.uint8, device=device)
         self.v = torch.zeros_like(self.k)
         self.k_scale = torch.zeros(num_phys_pages, num_kv_heads, dtype=torch.float32, device=device)
         self.v_scale = torch.zeros_like(self.k_scale)
@@ -158,18 +159,22 @@ class DeltaStack:
         if self.cache is None:
             N.kv_append_layers(self.desc, self.pt, k_new[a:b], v_new[a:b], k_pools[a:b], v_pools[a:b], st)
         else:
-            self._check_pools(k_pools[a:b])
             N.kv_append_layers_q8(self.desc, self.pt, k_new[a:b], v_new[a:b], [x.c for x in k_pools[a:b]], st)
 
     def _check_pools(self, pools):
+        """Every layer's pools, before a step launches anything (the kernels read as many pages as desc names)."""
+        if self.cache is None:
+            return
+        d = self.desc
+        shape = (d.num_phys_pages, d.num_kv_heads, 16, d.head_dim)
         for x in pools:
-            if not isinstance(x, Q8Pools) or x.format != self.cache or tuple(x.k.shape) != (
-                    self.desc.num_phys_pages, self.desc.num_kv_heads, 16, self.desc.head_dim):
+            if not isinstance(x, Q8Pools) or x.format != self.cache or x.shape != shape:
                 raise ValueError(f"a stack with a {self.cache} cache takes Q8Pools of its format and shape")
 
     def step(self, q, k_new, v_new, k_pools, v_pools, out, append: bool = True, stream: int | None = None):
         st = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
         cur = -1
+        self._check_pools(k_pools)
         q, k_new = self._rotate(q, k_new, 0, len(self.kinds), st)
         if append:
             self._append(k_new, v_new, k_pools, v_pools, 0, len(self.kinds), st)
@@ -196,6 +201,7 @@ class DeltaStack:
         Everything is enqueued on the current stream (graph-capturable); out_host is complete once
         that stream reaches the end of the step.
         """
+        self._check_pools(k_pools)
         main = torch.cuda.current_stream(self.device)
         if not hasattr(self, "_up"):
             self._up = torch.cuda.Stream(self.device)
@@ -296,6 +302,7 @@ class DeltaStack:
         """
         st = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
         L = len(self.kinds)
+        self._check_pools(k_pools)
         q, _ = self._rotate(q, None, 0, L, st)
         scores = torch.zeros(L, self.batch, self.max_pages, dtype=torch.float32, device=self.device)
         shift = torch.zeros(L, self.batch, dtype=torch.float32, device=self.device)

@@ -86,3 +86,25 @@ def test_nothing_between_the_layers_keeps_the_settled_entry(calls):
     # without an append and without rotary positions the second group's first layer stands behind a layer too
     run(["delta", "sparse", "sparse", "sparse"], None, True, append=False, early_layers=2)
     assert calls == ["select_attn", "sparse_attn", "sparse_attn_settled", "sparse_attn_settled"]
+
+
+@pytest.mark.parametrize("how", ["step", "step without append", "host", "host without append", "calibration"])
+@pytest.mark.parametrize("bad", [dict(format="e4m3"), dict(num_phys_pages=2), dict(num_kv_heads=3), dict(head_dim=128), None])
+def test_pools_of_another_format_or_shape_are_refused(calls, how, bad):
+    # (a pool of fewer pages than the stack's descriptor names would be read past its end)
+    kinds = ["full", "delta", "sparse"]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    stack = S.DeltaStack(kinds, 4, 2, 64, torch.bfloat16, i32(0, 1), i32(0), i32(9), 1, 3, 4, cache="int8")
+    new = lambda h: torch.zeros(3, 1, h, 64, dtype=torch.bfloat16)  # noqa: E731
+    good = dict(num_phys_pages=3, num_kv_heads=2, head_dim=64, format="int8", device="cpu")
+    pools = [S.Q8Pools(**good) for _ in kinds]
+    pools[1] = "text" if bad is None else S.Q8Pools(**{**good, **bad})
+    with pytest.raises(ValueError):
+        if how == "calibration":
+            stack.calibration_shifts(new(4), pools, None, new(4))
+        elif how.startswith("host"):
+            stack.step_host(new(4), new(2), new(2), pools, None, new(4), new(4), new(2), new(2), new(4),
+                            append="without" not in how)
+        else:
+            stack.step(new(4), new(2), new(2), pools, None, new(4), append="without" not in how)
+    assert calls == []                  # before anything is launched
