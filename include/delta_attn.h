@@ -255,7 +255,9 @@ typedef enum { DELTA_ROPE_HALF = 0, DELTA_ROPE_INTERLEAVED = 1 } delta_rope_layo
  *   DELTA_ROPE_LINEAR  f_j / factor (every position is divided by factor)
  *   DELTA_ROPE_BANDS   by the turns r_j = original_len * f_j / (2 pi) a pair makes over the trained
  *                      context: f_j / factor below low_turns, f_j above high_turns, mixed linearly
- *                      in r_j between (w f_j + (1 - w) f_j / factor, w = (r_j - low) / (high - low)) */
+ *                      in r_j between (w f_j + (1 - w) f_j / factor, w = (r_j - low) / (high - low))
+ * Other published forms (a ramp linear in the pair's index instead of its turns, factors of each pair) are
+ * tables that delta_rope_table does not make: delta_rope takes any table of turns. */
 typedef enum { DELTA_ROPE_PLAIN = 0, DELTA_ROPE_LINEAR = 1, DELTA_ROPE_BANDS = 2 } delta_rope_scaling;
 
 typedef struct {

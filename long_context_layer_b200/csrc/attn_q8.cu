@@ -37,8 +37,8 @@ SplitPlan plan_q8_variant(int D, int batch, int Hkv, int items, int variant) {
 }
 
 // One wide CTA an SM where plan_splits has one for the bf16 cache, by the same rules: a full cluster for each of a
-// few units with long lists (one sequence: 8k full layer 7.7 instead of 8.3 us, 32k 20 instead of 24.5), and
-// mid-size batches (4 x 64k 84 instead of 91 us, 2 x 4k 8.6 instead of 10.6); else two narrow ones.
+// few units with long lists (one sequence: 8k full layer 7.2 instead of 7.6 us, 32k 14.5 instead of 18), and
+// mid-size batches (4 x 64k 86 instead of 87 us, its delta-layer 99 instead of 119); else two narrow ones.
 SplitPlan plan_q8(int dtype, int D, int batch, int Hkv, int items) {
     const int64_t units = int64_t(batch) * Hkv;
     const int sms = device_sm_count();

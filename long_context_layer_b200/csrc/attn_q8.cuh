@@ -8,9 +8,9 @@ namespace delta {
 
 // Narrow CTAs, two an SM (kVarNarrow), or, bf16 queries, one CTA of twice the warps an SM (kVarWide).  A warp's ring
 // holds 4 pages: while a pair of pages is worked on, the next pair is on its way.  head_dim 128: 6 warps, 96 KB a
-// CTA (8 warps with 3 pages: 16 x 16k sparse layer 20 instead of 18.6 us, full layers alike).  head_dim 64: the
-// pages are half as large for nearly the same work, so 8 warps (16 x 16k full layer 51 us; 6 warps with 8 pages
-// 60, 10 warps 52).
+// CTA (8 warps with 3 pages: 16 x 16k full layer 97 instead of 84 us, sparse 22 instead of 19).  head_dim 64: the
+// pages are half as large for nearly the same work, so 8 warps (16 x 16k full layer 58 us; 6 warps with 8 pages
+// 66, 10 warps 76).
 constexpr int q8_warps(int D, bool wide) { return (D == 128 ? 6 : 8) * (wide ? 2 : 1); }
 constexpr int kQ8Stages = 4;
 

@@ -9,11 +9,11 @@
 //        4-byte register of an ldmatrix row holds two 2-value fragments of one token, dimensions 4 t4 + {0, 1}
 //        and 4 t4 + {2, 3} of a 16-byte chunk; the product sums over dimensions, so their order is free as long
 //        as Q's fragments follow it.  (The 8-bit mma.m16n8k32 over e4m3 operands is executed as two fp16
-//        products with conversions of both operands: 115 instead of 104 us for the delta-layer of 16 x 16k.)
+//        products with conversions of both operands, a tenth slower for the delta-layer of 16 x 16k.)
 //        int8: the payload is an operand of mma.m16n8k32 over bytes, and a query is 23-bit fixed point, its high
 //        bytes (signed), middle and low bytes (unsigned) on three integer accumulators: exact down to 2^-14 of
-//        the head's largest element, the others to 2^-22 of it.  No conversion of K (84 us for 4 x 64k,
-//        91 in fp16).  Two bytes would do for even queries and save 2 to 6 % where lists are short, but leave
+//        the head's largest element, the others to 2^-22 of it.  No conversion of K (4 x 64k 86 us,
+//        in fp16 91; 16 x 16k 84 and 90).  Two bytes would do for even queries and save 2 to 6 % where lists are short, but leave
 //        2^-15 of the largest element, which queries with an outlying dimension would show.
 //        fp32 queries: the fp16 form with a query as the sum of two values (22 bits and the sign).
 //   s = S * (Q's factor per head) * (K's block scale): powers of two and the softmax scale, in fp32.
@@ -25,8 +25,8 @@
 //        two dimensions of one token; a byte permute separates them, and the accumulator's rows g4 and g4 + 8
 //        are dimensions 2 g4 and 2 g4 + 1 of the 16-dimension tile.
 // Block scales range over 2^-100..2^122: K's multiplies the logits; V's joins P relative to the accumulators' unit,
-// the largest scale so far.  (Scaling the product instead costs 64 multiply-adds a pair of pages: about a third
-// of the pages of caches with ordinary spread differ from the unit, 310 instead of 267 instructions a page.)
+// the largest scale so far.  (Scaling the product instead costs 64 multiply-adds a pair of pages, and about a third of
+// the pages of caches with ordinary spread differ from the unit.)
 #pragma once
 
 #include "decode_mma.cuh"

@@ -222,8 +222,8 @@ inline int max_active_clusters(const void* func, size_t smem, int cluster, int t
 // (sequence, KV head) unit in one cluster, so each CTA gets the unit's per-head normalisers from the
 // cluster merge (a unit spread over several clusters needs a second arrival stage).
 // spare: clusters that must stay free.  A plan that takes every place can end in two waves behind a kernel that is
-// still draining: 56 units in clusters of 5 on 8-bit layers, 111 instead of 93 us (full) and 151 instead of 101
-// (delta-layer) against the next smaller clusters.
+// still draining: 56 units of 16k tokens in clusters of 5 on 8-bit layers, 56 instead of 44 us (full) and 75 instead of
+// 53 (delta-layer) against the next smaller clusters.
 // kernel_of(variant, &smem, &threads): the kernel of that variant, its dynamic shared memory and threads.
 template <typename KernelOf>
 SplitPlan fit_plan_now(SplitPlan pl, const KernelOf& kernel_of, int units, int items, bool one_cluster_per_unit,

@@ -5,8 +5,8 @@
 // Bound: the bytes of the visible K and V; the pages at the window's start and the sinks' end are read
 // whole, at most 30 tokens more.  The bf16 kernel carries each probability as two bf16 values (16 bits instead of
 // 8), which at a few percent of the tensor pipe costs no time that shows: 16 sequences of up to 32k tokens, a
-// window of 4,096 and 16 sinks, 40 query and 8 KV heads of 128 (215 MB of visible K and V) take 37 us, 5.8 TB/s;
-// one sequence with a window of 1,024 takes 4 us in a chain of such layers, latency.
+// window of 4,096 and 16 sinks, 40 query and 8 KV heads of 128 (215 MB of visible K and V) take 37 to 38 us, 5.7 TB/s;
+// one sequence with a window of 1,024 takes 4.1 us in a graph of such layers, latency.
 
 #include "host.cuh"
 #include "launch_plain.cuh"
