@@ -177,8 +177,9 @@ delta_status delta_full_attn(const delta_desc* desc, const delta_page_table* pt,
  *
  * Same inputs, output and results as delta_full_attn.  Its scratch is a fixed 8 MiB array
  * inside the library (static device memory: every GPU that loads the library keeps it until
- * the process exits).  The call allocates and frees nothing.  Shapes whose
- * delta_workspace_size() exceeds 8 MiB return DELTA_ERR_UNSUPPORTED.
+ * the process exits).  The call allocates and frees nothing.  Shapes whose counters and
+ * scratch exceed 8 MiB return DELTA_ERR_UNSUPPORTED (none does whose delta_workspace_size()
+ * is within 8 MiB: a workspace has room besides for what delta-layers keep in it).
  * - The first call on a device looks up the array's device address (cudaGetSymbolAddress)
  *   with that device current; make that first call before any stream capture.
  * - All calls share the one array and it keeps the last call's contents: each call clears

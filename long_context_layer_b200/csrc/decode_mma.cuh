@@ -493,13 +493,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_mma_kernel(const DecodeP
     constexpr int kPart = STAGES * int(S::kPage) / 4;     // floats between two warps' records
     const float* mo0 = reinterpret_cast<const float*>(smem);
     float pre[2][G];   // delta-layers: this CTA's page terms, loaded before the merge
-    int flags = 0;
-    if (!WIN && p.fuse_select) flags = select_preload<WARPS * 32, G>(p, b, g, ex.N, pre);
+    if (!WIN && p.fuse_select) select_preload<WARPS * 32, G>(p, b, g, ex.N, pre);
     merge_epilogue<__nv_bfloat16, D, G, WARPS, WARPS * 32, kRow>(
         p, smem, mo0, mo0 + kMaxGroup * kRow, recv, b, g, kPart, kPart,
         (!WIN && p.mode == kModeDelta) ? mo0 + kMaxGroup * kRow + kMaxGroup * 2 : nullptr);
     // delta-layers scoring with HEAD_SUM: page scores and the selection, in the stage area
-    if (!WIN && p.fuse_select) select_tail<WARPS * 32, G, D>(p, smem, S::kStages, recv, b, g, ex.n, ex.N, pre, flags);
+    if (!WIN && p.fuse_select) select_tail<WARPS * 32, G, D>(p, smem, S::kStages, recv, b, g, ex.n, ex.N, pre);
 }
 
 }  // namespace delta

@@ -698,11 +698,10 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1) decode_q8_kern
     constexpr int kPart = STAGES * int(S::kPage2) / 4;    // floats between two warps' records
     const float* mo0 = reinterpret_cast<const float*>(smem);
     float pre[2][G];   // delta-layers: this CTA's page terms, loaded before the merge
-    int flags = 0;
-    if (p.fuse_select) flags = select_preload<WARPS * 32, G>(p, b, g, ex.N, pre);
+    if (p.fuse_select) select_preload<WARPS * 32, G>(p, b, g, ex.N, pre);
     merge_epilogue<T, D, G, WARPS, WARPS * 32, kRow>(
         p, smem, mo0, mo0 + kMaxGroup * kRow, recv, b, g, kPart, kPart);
-    if (p.fuse_select) select_tail<WARPS * 32, G, D>(p, smem, S::kStages, recv, b, g, ex.n, ex.N, pre, flags);
+    if (p.fuse_select) select_tail<WARPS * 32, G, D>(p, smem, S::kStages, recv, b, g, ex.n, ex.N, pre);
 }
 
 }  // namespace delta

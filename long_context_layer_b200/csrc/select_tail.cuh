@@ -30,6 +30,10 @@ constexpr float kFixInv = 2.7755575615628914e-17f;  // 2^-55
 
 // What the sequence's last CTA needs (passed by value to the non-inlined final stage).
 struct SelectFinal {
+    const int32_t* indptr;
+    const int32_t* indices;
+    int64_t num_phys_pages;
+    const int* err;
     unsigned long long* score_acc;   // [B][max_pages]
     uint32_t* keys;                  // [B][max_pages]
     float* page_scores;              // [B][max_pages] or null
@@ -61,10 +65,9 @@ __device__ __forceinline__ bool arrive_last(int* counter, int expected, uint32_t
 
 // Delta-layers, one cluster per unit: this CTA's page terms lse_hj for its first 2 NTHR pages,
 // loaded right after the loop (its warps wrote them before the preceding block barrier) so that
-// their latency overlaps the output merge.  Returns the workspace's error flags (this CTA's own among them): a
-// skipped page has no terms, what stands there is an earlier launch's.
+// their latency overlaps the output merge.
 template <int NTHR, int G>
-__device__ __forceinline__ int select_preload(const DecodeParams& p, int b, int g, int N, float (&pre)[2][G]) {
+__device__ __forceinline__ void select_preload(const DecodeParams& p, int b, int g, int N, float (&pre)[2][G]) {
     const size_t maxp = size_t(p.max_pages);
     const float* pl = p.page_lse + (size_t(b) * p.num_q_heads + g * G) * maxp;
     const int i0 = blockIdx.x * p.items_per_split, i1 = min(i0 + p.items_per_split, N);
@@ -75,7 +78,6 @@ __device__ __forceinline__ int select_preload(const DecodeParams& p, int b, int 
             const int j = i0 + int(threadIdx.x) + i * NTHR;
             pre[i][h] = (j < i1) ? pl[size_t(h) * maxp + j] : -INFINITY;
         }
-    return __ldcg(p.err);
 }
 
 // Steps of the sequence's last CTA: page scores and their order keys, the threshold key T and the
@@ -106,6 +108,8 @@ __device__ __noinline__ void select_final(const SelectFinal a, unsigned char* sm
     const bool take_all = max(recStart - sinkP, 0) <= k;
     const bool radix = !take_all && k > 0;
     unsigned long long* acc = a.score_acc + size_t(b) * maxp;
+    // some page was skipped: such pages score 0 (their terms are an earlier launch's)
+    const bool skipped = (__ldcg(a.err) & kErrPage) != 0;
     uint32_t kmin = 0xffffffffu, kmax = 0u;
     for (int jb = tid; jb < N; jb += 16 * NTHR) {
         unsigned long long v[16];
@@ -119,7 +123,8 @@ __device__ __noinline__ void select_final(const SelectFinal a, unsigned char* sm
             const int j = jb + i * NTHR;
             if (j >= N) break;   // small contexts: most slots are empty
             acc[j] = 0ull;
-            const float sc = __ull2float_rn(v[i]) * kFixInv;
+            float sc = __ull2float_rn(v[i]) * kFixInv;
+            if (skipped && bad_entry(a, b, j)) sc = 0.f;
             if (a.page_scores != nullptr) a.page_scores[size_t(b) * maxp + j] = sc;
             const uint32_t key = order_key(sc);
             keys[j] = key;
@@ -342,11 +347,11 @@ __device__ __noinline__ void select_final(const SelectFinal a, unsigned char* sm
 
 // Every thread of the CTA calls this after the output merge.  smem: the kernel's page-stage area,
 // idle by now (free_bytes long, 16-byte aligned); recv: the merge's receive area; n, N: the
-// sequence's tokens and pages; pre, flags: select_preload's terms and flags.
+// sequence's tokens and pages; pre: select_preload's terms.
 template <int NTHR, int G, int D>
 __device__ __forceinline__ void select_tail(const DecodeParams& p, unsigned char* smem, size_t free_bytes,
                                             const float* recv, int b, int g, int n, int N,
-                                            const float (&pre)[2][G], int flags) {
+                                            const float (&pre)[2][G]) {
     const int tid = threadIdx.x;
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, S = p.num_splits, h0 = g * G;
     const size_t maxp = size_t(p.max_pages);
@@ -356,7 +361,6 @@ __device__ __forceinline__ void select_tail(const DecodeParams& p, unsigned char
     unsigned long long* acc = p.score_acc + size_t(b) * maxp;
     // adds the unit's share of page j's score (the sum over its G heads of 2^(lse_hj - c_h))
     auto add_share = [&](int j, const float (&v)[G]) {
-        if ((flags & kErrPage) && bad_entry(p, b, j)) return;     // a skipped page scores 0
         float sc = 0.f;
 #pragma unroll
         for (int h = 0; h < G; ++h) sc += exp2_approx(v[h] - s_c[h]);
@@ -405,6 +409,10 @@ __device__ __forceinline__ void select_tail(const DecodeParams& p, unsigned char
     shares(i0 + 2 * NTHR, i1);
     if (!arrive_last(p.seq_tickets + b, Hkv * S, s_flag)) return;
     SelectFinal a;
+    a.indptr = p.indptr;
+    a.indices = p.indices;
+    a.num_phys_pages = p.num_phys_pages;
+    a.err = p.err;
     a.score_acc = p.score_acc;
     a.keys = p.keys;
     a.page_scores = p.page_scores;
